@@ -23,7 +23,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libw8.so")
 
-SOURCES = ["w8_api.cu", "w8_gemv.cu", "w8_tc.cu", "w8_repack.cu", "w8_noalloc.cu"]
+SOURCES = ["w8_api.cu", "w8_gemv.cu", "w8_tc.cu", "w8_repack.cu", "w8_noalloc.cu",
+           "w8_serve_api.cu", "w8_paging.cu", "w8_latent_paged.cu", "w8_latent_expanded.cu",
+           "w8_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "-Xptxas", "-v", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -38,7 +40,7 @@ def _nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "w8.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("w8.h", "w8_serve.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
