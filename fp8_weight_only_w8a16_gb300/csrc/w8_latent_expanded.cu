@@ -69,6 +69,12 @@ __global__ void __launch_bounds__(256) expanded_kernel(const w8_latent_expanded 
 
 } // namespace
 
+cudaError_t expanded_status(int *out, bool)
+{
+    *out = 0;
+    return cudaSuccess;
+}
+
 cudaError_t launch_latent_expanded(const w8_latent_expanded &a, int, cudaStream_t s)
 {
     const int64_t rows = int64_t(a.n_q) * a.n_heads;

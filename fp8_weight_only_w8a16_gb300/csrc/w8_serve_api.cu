@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxStride = int64_t(1) << 38; // elements; tensor-map strides stay below 2^40 bytes
 constexpr int64_t kMaxItems = int64_t(1) << 30; // rows of an output, tokens, logits of a row
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -83,7 +83,11 @@ w8_status w8_serve_device_status(int *status, int reset)
 {
     if (!status)
         return W8_ERR_NULL;
-    return launched(w8::serve_status(status, reset != 0));
+    int paged = 0, expanded = 0;
+    if (w8::paged_status(&paged, reset != 0) != cudaSuccess || w8::expanded_status(&expanded, reset != 0) != cudaSuccess)
+        return W8_ERR_CUDA;
+    *status = (paged ? 1 : 0) | (expanded ? 2 : 0);
+    return W8_OK;
 }
 
 w8_status w8_block_tables(const int32_t *ctx_lens, const int32_t *new_lens, int n_req, int page_size,

@@ -55,8 +55,10 @@ struct LogprobsArgs {
 int logprobs_splits(int rows, int vocab, int sms);
 cudaError_t launch_logprobs(const LogprobsArgs &a, bool bf16, cudaStream_t s);
 
-// The attention kernels' status word (w8_serve_device_status).
-cudaError_t serve_status(int *out, bool reset);
+// The attention kernels' status words (w8_serve_device_status): not 0 once a
+// wait gave up.
+cudaError_t paged_status(int *out, bool reset);
+cudaError_t expanded_status(int *out, bool reset);
 
 // Launch with the programmatic-dependency attribute (the kernel waits for the
 // stream's previous kernel itself, before its first global access).
