@@ -23,9 +23,11 @@
 // MN-major for the second.  Rows of Q past the group read whatever follows
 // in shared memory: they make rows of S that nobody reads.
 //
-// Six warps: 0-3 softmax (16 rows each; loads S, writes P as bf16 into shared
+// Seven warps: 0-3 softmax (16 rows each; loads S, writes P as bf16 into shared
 // memory, raises the reference, divides and stores), 4 copies (tensor-map
-// boxes of min(page, 64) tokens x 64 columns), 5 tensor-core issue.  The ring
+// boxes of min(page, 64) tokens x 64 columns), 5 and 6 issue the two products
+// (a thread each: with one thread for both, a tile's second product waited
+// for the next tile's copies, 4.8 us a tile instead of XXX).  The ring
 // frees latent columns in units of 128 as the second product passes over
 // them; the rope chunk has a ring of its own and is free after the first.
 // The reference moves only when a row's maximum passes it by 2^8 (p stays
@@ -44,6 +46,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "w8_device.cuh"
 #include "w8_serve_internal.h"
@@ -61,7 +64,7 @@ constexpr int kTile = 64;                    // tokens
 constexpr int kChunk = kTile * 128;          // bytes of 64 tokens x 64 columns
 constexpr int kUnit = 2 * kChunk;            // 128 latent columns
 constexpr int kMaxRows = 64;
-constexpr int kPagedThreads = 192, kSoftThreads = 128, kCopyWarp = 4, kMmaWarp = 5;
+constexpr int kPagedThreads = 224, kSoftThreads = 128, kCopyWarp = 4, kScoreWarp = 5, kOutWarp = 6;
 constexpr int kMaxUnits = 12, kMaxRopes = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
@@ -172,41 +175,478 @@ struct Walk {
     }
 };
 
+// 2 KB at most: the rest is the rings'.
+struct Shared {
+    uint64_t unit_full[kMaxUnits], unit_free[kMaxUnits];
+    uint64_t rope_full[kMaxRopes], rope_free[kMaxRopes];
+    uint64_t q, s[2], s_free[2], p, o, end[2];
+    int64_t out[kMaxRows]; // a row's place in the output
+    int64_t sum[kPagedThreads / 32];
+    int max[kPagedThreads / 32];
+    int start[3];
+    uint32_t tmem;
+    float f[kMaxRows], inv[kMaxRows];
+};
+
+static_assert(sizeof(Shared) <= 227 * 1024 - kSmem, "shared memory");
+
+// A ring's next slot and the parity of its use.
+struct Turn {
+    int k = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void step(int slots)
+    {
+        if (++k == slots) {
+            k = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// One lane of a converged warp.  Tensor-core steps issued by a lane that the
+// compiler only knows as `lane == 0` take 85 to 130 cycles each whatever their
+// shape; issued under this they take their own 32 to 128.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Keys that the last row of the walk's group sees.
+__device__ __forceinline__ int group_sees(const w8_latent_paged &a, const Walk &w, int nr)
+{
+    return seen(w.req, (min((w.g + 1) * nr, w.req.q * a.n_heads) - 1) / a.n_heads);
+}
+
+// ---- copies ---------------------------------------------------------------
+template <int NR>
+__device__ __forceinline__ bool copy_role(const w8_latent_paged &a, const CUtensorMap &map, Walk w, uint8_t *sm, Shared &sh,
+                                          int lane)
+{
+    constexpr Smem lay = smem_plan(NR);
+    // lane l of a unit's copies: chunk l / boxes, box l % boxes
+    const int page = a.cache.page_size, box = min(page, kTile), boxes = kTile / box;
+    const int shift = 31 - __clz(page), bx = lane % boxes, c = lane / boxes;
+    Turn un, rn;
+    int units = 0, ropes = 0; // copied so far
+    bool ok = true;
+    for (bool first = true; ok && w.next(a, NR, first); first = false) {
+        const int32_t *table = a.block_table + int64_t(w.r) * a.ld_table;
+        const int vis = group_sees(a, w, NR);
+        // this lane's page of a tile; the next tile's is fetched ahead
+        auto page_of = [&](int t) {
+            const int j = t * kTile + bx * box;
+            int pg = a.cache.n_pages; // reads as zeros
+            if (t < w.off + w.run && j < vis) {
+                pg = __ldg(table + (j >> shift));
+                pg = pg < 0 || pg > a.cache.n_pages ? a.cache.n_pages : pg;
+            }
+            return pg;
+        };
+        int pg = page_of(w.off);
+        for (int t = w.off; ok && t < w.off + w.run; ++t) {
+            const int j0 = t * kTile, left = min(vis - j0, kTile);
+            if (left <= 0)
+                break;
+            const int need = (left + box - 1) / box; // boxes with a key that is seen
+            const int y = (j0 + bx * box) & (page - 1);
+            const int ahead = page_of(t + 1);
+            for (int u = 0; u < 5; ++u) {
+                const bool rope = u == 4;
+                const int k = rope ? rn.k : un.k;
+                uint64_t *full = rope ? &sh.rope_full[k] : &sh.unit_full[k];
+                if (rope ? ropes >= lay.ropes : units >= lay.units)
+                    ok = __all_sync(0xffffffffu, rope ? bar_wait(&sh.rope_free[k], rn.parity ^ 1)
+                                                      : bar_wait(&sh.unit_free[k], un.parity ^ 1));
+                if (!ok)
+                    break;
+                const int chunks = rope ? 1 : 2;
+                if (lane == 0)
+                    bar_expect(full, uint32_t(chunks * need * box * 128));
+                __syncwarp();
+                if (c < chunks && bx < need)
+                    copy_box(smem_addr(sm + (rope ? lay.rope + k * kChunk : lay.unit + k * kUnit) + c * kChunk + bx * box * 128),
+                             &map, 64 * (2 * u + c), y, pg, full);
+                if (rope) {
+                    rn.step(lay.ropes);
+                    ++ropes;
+                } else {
+                    un.step(lay.units);
+                    ++units;
+                }
+            }
+            pg = ahead;
+        }
+    }
+    // the copies still in flight (there are any only after a wait elsewhere gave up)
+    for (int i = max(0, units - lay.units); i < units; ++i)
+        bar_wait(&sh.unit_full[i % lay.units], uint32_t((i / lay.units) & 1));
+    for (int i = max(0, ropes - lay.ropes); i < ropes; ++i)
+        bar_wait(&sh.rope_full[i % lay.ropes], uint32_t((i / lay.ropes) & 1));
+    return ok;
+}
+
+// ---- first product ----------------------------------------------------------
+template <int NR>
+__device__ __forceinline__ bool score_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, uint32_t tm_s)
+{
+    constexpr Smem lay = smem_plan(NR);
+    constexpr uint32_t id = inst_desc(64, kTile, false, false);
+    const uint64_t dq = desc128_k(smem_addr(sm + lay.q), 1024);
+    const uint64_t drope = desc128_k(smem_addr(sm + lay.rope), 1024), dunit = desc128_k(smem_addr(sm + lay.unit), 1024);
+    const bool one = elect_one();
+    Turn un, rn;
+    int runs = 0, n = 0; // runs with keys, tiles
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, parity & 1)); };
+    for (bool first = true; ok && w.next(a, NR, first); first = false) {
+        if (group_sees(a, w, NR) == 0)
+            continue;
+        wait(&sh.q, uint32_t(runs));
+        ++runs;
+        for (int t = 0; ok && t < w.run; ++t, ++n) {
+            // S of tile n - 2, in the same columns, has been read
+            if (n >= 2)
+                wait(&sh.s_free[n & 1], uint32_t(n / 2 - 1));
+            const uint32_t d = tm_s + uint32_t(n & 1) * kTile;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                wait(&sh.unit_full[un.k], un.parity);
+                if (!ok)
+                    break;
+                fence_after();
+                const uint64_t dk = dunit + uint64_t((un.k * kUnit) >> 4);
+                if (one) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        mma_ss(d, dq + uint64_t(((2 * u + s / 4) * NR * 128 + (s % 4) * 32) >> 4),
+                               dk + uint64_t(((s / 4) * kChunk + (s % 4) * 32) >> 4), id, uint32_t(u | s));
+                }
+                __syncwarp();
+                un.step(lay.units);
+            }
+            wait(&sh.rope_full[rn.k], rn.parity);
+            if (!ok)
+                break;
+            fence_after();
+            const uint64_t dk = drope + uint64_t((rn.k * kChunk) >> 4);
+            if (one) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    mma_ss(d, dq + uint64_t((8 * NR * 128 + s * 32) >> 4), dk + uint64_t((s * 32) >> 4), id, 1);
+                commit(&sh.rope_free[rn.k]);
+                commit(&sh.s[n & 1]);
+            }
+            __syncwarp();
+            rn.step(lay.ropes);
+        }
+    }
+    // nothing of this warp's is in the tensor cores when the CTA frees its memory
+    if (one)
+        commit(&sh.end[0]);
+    __syncwarp();
+    return bar_wait(&sh.end[0], 0) && ok;
+}
+
+// ---- second product ---------------------------------------------------------
+template <int NR>
+__device__ __forceinline__ bool out_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, uint32_t tmem)
+{
+    constexpr Smem lay = smem_plan(NR);
+    constexpr uint32_t id = inst_desc(128, NR, true, false);
+    const uint64_t dp = desc128_k(smem_addr(sm + lay.p), 1024), dunit = desc128(smem_addr(sm + lay.unit), kChunk, 1024);
+    const bool one = elect_one();
+    Turn un;
+    int n = 0;
+    bool ok = true;
+    for (bool first = true; ok && w.next(a, NR, first); first = false) {
+        if (group_sees(a, w, NR) == 0)
+            continue;
+        for (int t = 0; ok && t < w.run; ++t, ++n) {
+            ok = __all_sync(0xffffffffu, bar_wait(&sh.p, uint32_t(n & 1)));
+            if (!ok)
+                break;
+            fence_after();
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint64_t dv = dunit + uint64_t((un.k * kUnit) >> 4);
+                if (one) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_ss(tmem + uint32_t(u * NR), dv + uint64_t((s * 2048) >> 4), dp + uint64_t((s * 32) >> 4), id,
+                               uint32_t(t | s));
+                    commit(&sh.unit_free[un.k]);
+                }
+                __syncwarp();
+                un.step(lay.units);
+            }
+            if (one)
+                commit(&sh.o);
+            __syncwarp();
+        }
+    }
+    if (one)
+        commit(&sh.end[1]);
+    __syncwarp();
+    return bar_wait(&sh.end[1], 0) && ok;
+}
+
+// ---- softmax, output --------------------------------------------------------
+template <int NR>
+__device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, uint32_t tmem,
+                                             uint32_t tm_s, const Parts &parts, int64_t total, int64_t ctas, int tid)
+{
+    constexpr Smem lay = smem_plan(NR);
+    const int warp = tid >> 5, lane = tid & 31;
+    const float sl = a.scale * kLog2e;
+    const int g4 = lane >> 2, t4 = lane & 3;
+    const bool active = 16 * warp < NR; // warps that have rows
+    const uint32_t lanes = uint32_t(32 * warp) << 16;
+    bool ok = true;
+    // a wait that gave up is followed by no other, but every barrier below is
+    // still met, so that no warp waits for one that left
+    auto wait = [&](uint64_t *bar, int phase) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, uint32_t(phase & 1))); };
+    if (tid == 0 && (w.pos >= w.end || w.off == 0))
+        parts.at[blockIdx.x].last = -1; // no group runs over this CTA's start
+    // the rows' places in Q, while Q is loaded, where P will be
+    int64_t *const q_at = reinterpret_cast<int64_t *>(sm + lay.p);
+    int n = 0; // tiles so far
+    for (bool first = true; w.next(a, NR, first); first = false) {
+        const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
+        const int vis = seen(w.req, (row0 + rows - 1) / a.n_heads);
+        // the two rows of this thread: how many keys they see
+        int lim[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = 16 * warp + g4 + 8 * h;
+            lim[h] = row < rows ? seen(w.req, (row0 + row) / a.n_heads) : 0;
+        }
+        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, z[2] = {0.0f, 0.0f};
+        if (tid < rows) {
+            const int tok = w.req.q0 + (row0 + tid) / a.n_heads, head = (row0 + tid) % a.n_heads;
+            sh.out[tid] = tok * a.ld_out_tok + head * a.ld_out_head;
+            q_at[tid] = tok * a.ld_qlat_tok + head * a.ld_qlat_head;
+            q_at[NR + tid] = tok * a.ld_qrope_tok + head * a.ld_qrope_head;
+        }
+        sync_some(1, kSoftThreads);
+        if (vis > 0) {
+            // Q: 72 vectors of 16 bytes a row, nine loads of a thread in flight
+            constexpr int kBatch = 9;
+#pragma unroll 1
+            for (int i0 = 0; i0 < NR * 72; i0 += kBatch * kSoftThreads) {
+                uint4 x[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int i = i0 + b * kSoftThreads + tid, row = i / 72, v = i - row * 72;
+                    x[b] = make_uint4(0, 0, 0, 0);
+                    if (row < rows)
+                        x[b] = __ldg(reinterpret_cast<const uint4 *>(v < 64 ? a.q_lat + q_at[row] + 8 * v
+                                                                            : a.q_rope + q_at[NR + row] + 8 * (v - 64)));
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int i = i0 + b * kSoftThreads + tid, row = i / 72, v = i - row * 72;
+                    *reinterpret_cast<uint4 *>(sm + lay.q + (v >> 3) * NR * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)) =
+                        x[b];
+                }
+            }
+            fence_async_shared();
+            bar_arrive(&sh.q);
+            for (int t = 0; t < w.run; ++t, ++n) {
+                const int j0 = (w.off + t) * kTile;
+                wait(&sh.s[n & 1], n >> 1);
+                fence_after();
+                float f[2] = {1.0f, 1.0f};
+                float x[32];
+                bool raise = false;
+                if (active) {
+                    ld16x64(x, tm_s + lanes + uint32_t(n & 1) * kTile);
+                    wait_ld();
+                }
+                fence_before();
+                bar_arrive(&sh.s_free[n & 1]);
+                if (active) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (j0 + kTile > lim[h]) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (j0 + 8 * (i >> 1) + 2 * t4 + (i & 1) >= lim[h])
+                                    x[4 * (i >> 1) + 2 * h + (i & 1)] = -CUDART_INF_F;
+                        }
+                        float mx = x[2 * h];
+#pragma unroll
+                        for (int i = 1; i < 16; ++i)
+                            mx = fmaxf(mx, x[4 * (i >> 1) + 2 * h + (i & 1)]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        mx *= sl;
+                        if (m[h] == -CUDART_INF_F) {
+                            m[h] = mx; // nothing summed yet
+                        } else if (mx > m[h] + kRaise) {
+                            f[h] = ex2(m[h] - mx);
+                            m[h] = mx;
+                            z[h] *= f[h];
+                            raise = true;
+                        }
+                        const float ref = m[h] == -CUDART_INF_F ? 0.0f : m[h];
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float &e = x[4 * (i >> 1) + 2 * h + (i & 1)];
+                            e = ex2(fmaf(e, sl, -ref));
+                            sum += e;
+                        }
+                        z[h] += sum;
+                    }
+                }
+                // the last tile's second product has read P and written O
+                if (t > 0)
+                    wait(&sh.o, n - 1);
+                if (active) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = 16 * warp + g4 + 8 * h;
+                        uint8_t *p = sm + lay.p + row * 128 + 4 * t4;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint32_t *>(p + ((j ^ (row & 7)) << 4)) =
+                                pack_bf16(x[4 * j + 2 * h], x[4 * j + 2 * h + 1]);
+                        if (t4 == 0)
+                            sh.f[row] = f[h];
+                    }
+                }
+                if (j0 + kTile > vis) {
+                    // rows of the tile that nobody sees may hold anything: their weights are 0, 0 x NaN is not
+                    const int dead = kTile - (vis - j0);
+                    for (int i = tid; i < dead * 64; i += kSoftThreads) {
+                        const int c = i / (dead * 8), rest = i - c * dead * 8;
+                        const int k = (4 * n + c / 2) % lay.units;
+                        *reinterpret_cast<uint4 *>(sm + lay.unit + k * kUnit + (c & 1) * kChunk + (vis - j0) * 128 +
+                                                   rest * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (sync_any(1, kSoftThreads, raise)) {
+                    fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < NR / 4; ++c) { // 16 columns: rows 16 c % NR .. of block 16 c / NR
+                        float o[16];
+                        ld32x16(o, tmem + lanes + uint32_t(16 * c));
+                        wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] *= sh.f[(16 * c) % NR + i];
+                        st32x16(tmem + lanes + uint32_t(16 * c), o);
+                    }
+                    wait_st();
+                }
+                fence_before();
+                fence_async_shared();
+                bar_arrive(&sh.p);
+            }
+            wait(&sh.o, n - 1);
+            fence_after();
+        }
+        // ---- the run's result: the output, or a part of it
+        const bool whole = w.off == 0 && w.run == w.tiles;
+        const int slot = 2 * int(blockIdx.x) + (w.off == 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            z[h] += __shfl_xor_sync(0xffffffffu, z[h], 1);
+            z[h] += __shfl_xor_sync(0xffffffffu, z[h], 2);
+            const int row = 16 * warp + g4 + 8 * h;
+            if (active && t4 == 0) {
+                const bool some = z[h] > 0.0f || z[h] != z[h];
+                sh.inv[row] = some ? 1.0f / z[h] : 0.0f;
+                if (row < rows) {
+                    if (!whole)
+                        parts.mz[slot * kMaxRows + row] = make_float2(m[h], z[h]);
+                    else if (a.lse)
+                        a.lse[int64_t(w.req.q0) * a.n_heads + row0 + row] =
+                            some ? (m[h] + log2f(z[h])) * kLn2 : -CUDART_INF_F;
+                }
+            }
+        }
+        if (w.off > 0 && tid == 0) {
+            // the group runs over this CTA's start
+            const int64_t s0 = w.pos - w.off, s1 = s0 + w.tiles - 1; // the group's tiles in the line
+            Boundary b;
+            b.first = int(((s0 + 1) * ctas - 1) / total);
+            b.last = int(((s1 + 1) * ctas - 1) / total);
+            b.row0 = w.req.q0 * a.n_heads + row0;
+            b.rows = rows;
+            b.first_slot = 2 * b.first + 1;
+            parts.at[blockIdx.x] = b;
+        }
+        sync_some(1, kSoftThreads);
+#pragma unroll 1
+        for (int c = 0; c < NR / 4; ++c) {
+            const int n0 = (16 * c) % NR, d0 = 128 * (16 * c / NR) + 32 * warp;
+            if (n0 >= rows)
+                continue;
+            float o[16];
+            if (vis > 0) {
+                ld32x16(o, tmem + lanes + uint32_t(16 * c));
+                wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i] = 0.0f;
+            }
+            if (whole) {
+                // lane pairs trade halves, so that each stores two columns of one row
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float e = o[i] * sh.inv[n0 + i], d = o[i + 1] * sh.inv[n0 + i + 1];
+                    const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? e : d, 1);
+                    const int row = n0 + i + (lane & 1);
+                    if (row < rows)
+                        *reinterpret_cast<uint32_t *>(a.out + sh.out[row] + d0 + (lane & ~1)) =
+                            lane & 1 ? pack_bf16(got, d) : pack_bf16(e, got);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (n0 + i < rows)
+                        parts.o[(size_t(slot) * kMaxRows + n0 + i) * W8_LATENT_DIM + d0 + lane] = o[i];
+            }
+        }
+        fence_before(); // the loads of O, before the next run's products
+        sync_some(1, kSoftThreads); // the rows' places and 1 / z are read
+    }
+    return ok;
+}
+
 __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_kernel(const __grid_constant__ w8_latent_paged a, const __grid_constant__ CUtensorMap map, void *ws)
 {
     extern __shared__ __align__(16) uint8_t s_dyn[];
-    __shared__ __align__(8) uint64_t b_unit_full[kMaxUnits], b_unit_free[kMaxUnits];
-    __shared__ __align__(8) uint64_t b_rope_full[kMaxRopes], b_rope_free[kMaxRopes];
-    __shared__ __align__(8) uint64_t b_q, b_s[2], b_p, b_o, b_end;
-    __shared__ uint32_t s_tmem;
-    __shared__ int64_t s_sum[kPagedThreads / 32];
-    __shared__ int s_max[kPagedThreads / 32];
-    __shared__ int s_start[3];
-    __shared__ int64_t s_out[kMaxRows]; // a row's place in the output
-    __shared__ float s_f[kMaxRows], s_z[kMaxRows];
-
+    __shared__ __align__(16) Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *const sm = s_dyn + ((1024u - (smem_addr(s_dyn) & 1023u)) & 1023u);
     if (tid == 0) {
         for (int i = 0; i < kMaxUnits; ++i) {
-            bar_init(&b_unit_full[i], 1);
-            bar_init(&b_unit_free[i], 1);
+            bar_init(&sh.unit_full[i], 1);
+            bar_init(&sh.unit_free[i], 1);
         }
         for (int i = 0; i < kMaxRopes; ++i) {
-            bar_init(&b_rope_full[i], 1);
-            bar_init(&b_rope_free[i], 1);
+            bar_init(&sh.rope_full[i], 1);
+            bar_init(&sh.rope_free[i], 1);
         }
-        bar_init(&b_q, kSoftThreads);
-        bar_init(&b_s[0], 1);
-        bar_init(&b_s[1], 1);
-        bar_init(&b_p, kSoftThreads);
-        bar_init(&b_o, 1);
-        bar_init(&b_end, 1);
+        bar_init(&sh.q, kSoftThreads);
+        bar_init(&sh.s[0], 1);
+        bar_init(&sh.s[1], 1);
+        bar_init(&sh.s_free[0], kSoftThreads);
+        bar_init(&sh.s_free[1], kSoftThreads);
+        bar_init(&sh.p, kSoftThreads);
+        bar_init(&sh.o, 1);
+        bar_init(&sh.end[0], 1);
+        bar_init(&sh.end[1], 1);
         bar_init_fence();
     }
     if (warp == 0)
-        tmem_alloc(&s_tmem, kTmemCols);
+        tmem_alloc(&sh.tmem, kTmemCols);
     pdl_wait();
 
     // ---- the line of tiles: its length, NR, this CTA's run -------------------
@@ -233,17 +673,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         __syncthreads(); // the last pass's sums are read
         if (lane == 31) {
-            s_sum[warp] = inc;
-            s_max[warp] = rows;
+            sh.sum[warp] = inc;
+            sh.max[warp] = rows;
         }
         __syncthreads();
         before = inc - mine;
         total = 0;
         rows = 0;
         for (int w = 0; w < kPagedThreads / 32; ++w) {
-            before += w < warp ? s_sum[w] : 0;
-            total += s_sum[w];
-            rows = max(rows, s_max[w]);
+            before += w < warp ? sh.sum[w] : 0;
+            total += sh.sum[w];
+            rows = max(rows, sh.max[w]);
         }
         // fewer rows a group: when no group would be filled, or when that
         // many more groups still leave no SM two tiles
@@ -253,7 +693,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         nr = half;
     }
     const int64_t ctas = min(total, int64_t(gridDim.x)); // those that have work
-    const Smem lay = smem_plan(nr);
     Walk w{};
     w.pos = ctas ? min(int64_t(blockIdx.x), ctas) * total / ctas : 0;
     w.end = ctas ? min(int64_t(blockIdx.x) + 1, ctas) * total / ctas : 0;
@@ -265,9 +704,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             for (int g = 0; g < n; ++g) {
                 const int t = group_tiles(q, a.n_heads, nr, g);
                 if (at <= w.pos && w.pos < at + t) {
-                    s_start[0] = r;
-                    s_start[1] = g;
-                    s_start[2] = int(w.pos - at);
+                    sh.start[0] = r;
+                    sh.start[1] = g;
+                    sh.start[2] = int(w.pos - at);
                 }
                 at += t;
             }
@@ -276,323 +715,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = s_tmem, tm_s = tmem + 4 * kMaxRows; // O in columns 0 .., S after it
-    w.r = s_start[0];
-    w.g = s_start[1];
-    w.off = s_start[2];
-
+    const uint32_t tmem = sh.tmem, tm_s = tmem + 4 * kMaxRows; // O in columns 0 .., S after it
+    w.r = sh.start[0];
+    w.g = sh.start[1];
+    w.off = sh.start[2];
     const Parts parts = parts_of(ws, int(gridDim.x));
-    bool ok = true;
-    if (warp == kCopyWarp) {
-        // ---- copies --------------------------------------------------------------
-        // lane l of a unit's copies: chunk l / boxes, box l % boxes
-        const int page = a.cache.page_size, box = min(page, kTile), boxes = kTile / box;
-        int nu = 0, nc = 0; // units and rope chunks so far
-        for (bool first = true; ok && w.next(a, nr, first); first = false) {
-            const int32_t *table = a.block_table + int64_t(w.r) * a.ld_table;
-            const int vis = seen(w.req, (min((w.g + 1) * nr, w.req.q * a.n_heads) - 1) / a.n_heads);
-            for (int t = w.off; ok && t < w.off + w.run; ++t) {
-                const int j0 = t * kTile, left = min(vis - j0, kTile);
-                if (left <= 0)
-                    break;
-                const int need = (left + box - 1) / box; // boxes with a key that is seen
-                // this lane's box (the same one for every chunk it copies)
-                const int bx = lane % boxes;
-                int pg = 0;
-                if (bx < need) {
-                    pg = __ldg(table + (j0 + bx * box) / page);
-                    pg = pg < 0 || pg >= a.cache.n_pages ? a.cache.n_pages : pg;
-                }
-                const int y = (j0 + bx * box) % page;
-                for (int u = 0; ok && u < 5; ++u) {
-                    const bool rope = u == 4;
-                    const int k = rope ? nc % lay.ropes : nu % lay.units;
-                    const int round = rope ? nc / lay.ropes : nu / lay.units;
-                    uint64_t *full = rope ? &b_rope_full[k] : &b_unit_full[k];
-                    uint64_t *free_ = rope ? &b_rope_free[k] : &b_unit_free[k];
-                    if (round > 0)
-                        ok = __all_sync(0xffffffffu, bar_wait(free_, uint32_t((round - 1) & 1)));
-                    if (!ok)
-                        break;
-                    const int chunks = rope ? 1 : 2;
-                    if (lane == 0)
-                        bar_expect(full, uint32_t(chunks * need * box * 128));
-                    __syncwarp();
-                    const int c = lane / boxes;
-                    if (c < chunks && bx < need)
-                        copy_box(smem_addr(sm + (rope ? lay.rope + k * kChunk : lay.unit + k * kUnit) + c * kChunk + bx * box * 128),
-                                 &map, 64 * (2 * u + c), y, pg, full);
-                    rope ? ++nc : ++nu;
-                }
-            }
-        }
-        // the copies still in flight (only after a wait elsewhere gave up are there any)
-        for (int i = max(0, nu - lay.units); i < nu; ++i)
-            bar_wait(&b_unit_full[i % lay.units], uint32_t((i / lay.units) & 1));
-        for (int i = max(0, nc - lay.ropes); i < nc; ++i)
-            bar_wait(&b_rope_full[i % lay.ropes], uint32_t((i / lay.ropes) & 1));
-    } else if (warp == kMmaWarp) {
-        // ---- tensor-core steps: one thread ------------------------------------------
-        if (lane == 0) {
-            const uint32_t id_s = inst_desc(64, kTile, false, false), id_o = inst_desc(128, nr, true, false);
-            const uint64_t dq = desc128_k(smem_addr(sm + lay.q), 1024), dp = desc128_k(smem_addr(sm + lay.p), 1024);
-            const uint32_t rope0 = smem_addr(sm + lay.rope), unit0 = smem_addr(sm + lay.unit);
-            int nq = 0, n = 0;    // runs with keys, tiles finished
-            int su = 0, sc = 0;   // units and rope chunks of the first product
-            int ou = 0;           // units of the second
-            for (bool first = true; ok && w.next(a, nr, first); first = false) {
-                const int vis = seen(w.req, (min((w.g + 1) * nr, w.req.q * a.n_heads) - 1) / a.n_heads);
-                if (vis == 0)
-                    continue;
-                ok = bar_wait(&b_q, uint32_t(nq & 1));
-                ++nq;
-                fence_after();
-                auto scores = [&](int i) { // S of the CTA's i-th tile
-                    const uint32_t d = tm_s + uint32_t(i & 1) * kTile;
-                    for (int u = 0; ok && u < 4; ++u, ++su) {
-                        const int k = su % lay.units;
-                        ok = bar_wait(&b_unit_full[k], uint32_t((su / lay.units) & 1));
-                        if (!ok)
-                            return;
-                        const uint64_t dk = desc128_k(unit0 + k * kUnit, 1024);
-#pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            mma_ss(d, dq + uint64_t(((2 * u + s / 4) * nr * 128 + (s % 4) * 32) >> 4),
-                                   dk + uint64_t(((s / 4) * kChunk + (s % 4) * 32) >> 4), id_s, uint32_t(u | s));
-                    }
-                    const int k = sc % lay.ropes;
-                    ok = ok && bar_wait(&b_rope_full[k], uint32_t((sc / lay.ropes) & 1));
-                    if (!ok)
-                        return;
-                    const uint64_t dk = desc128_k(rope0 + k * kChunk, 1024);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_ss(d, dq + uint64_t((8 * nr * 128 + s * 32) >> 4), dk + uint64_t((s * 32) >> 4), id_s, 1);
-                    commit(&b_rope_free[k]);
-                    commit(&b_s[i & 1]);
-                    ++sc;
-                };
-                scores(n);
-                for (int t = 0; ok && t < w.run; ++t, ++n) {
-                    if (t + 1 < w.run)
-                        scores(n + 1);
-                    ok = ok && bar_wait(&b_p, uint32_t(n & 1));
-                    if (!ok)
-                        break;
-                    fence_after();
-                    for (int u = 0; u < 4; ++u, ++ou) {
-                        const int k = ou % lay.units;
-                        const uint64_t dv = desc128(unit0 + k * kUnit, kChunk, 1024);
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma_ss(tmem + uint32_t(u * nr), dv + uint64_t((s * 2048) >> 4), dp + uint64_t((s * 32) >> 4),
-                                   id_o, uint32_t(t | s));
-                        commit(&b_unit_free[k]);
-                    }
-                    commit(&b_o);
-                }
-            }
-            // nothing of this CTA's is in the tensor cores when it frees its memory
-            commit(&b_end);
-            ok = bar_wait(&b_end, 0) && ok;
-        }
-    } else {
-        // ---- softmax, output ------------------------------------------------------------
-        const float sl = a.scale * kLog2e;
-        const int g4 = lane >> 2, t4 = lane & 3;
-        const bool active = 16 * warp < nr; // warps that have rows
-        const uint32_t lanes = uint32_t(32 * warp) << 16;
-        // a wait that gave up is followed by no other, but every barrier below
-        // is still met, so that no warp waits for one that left
-        auto wait = [&](uint64_t *bar, int phase) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, uint32_t(phase & 1))); };
-        if (tid == 0 && (w.pos >= w.end || w.off == 0))
-            parts.at[blockIdx.x].last = -1; // no group runs over this CTA's start
-        int n = 0; // tiles so far
-        for (bool first = true; w.next(a, nr, first); first = false) {
-            const int row0 = w.g * nr, rows = min(nr, w.req.q * a.n_heads - row0);
-            const int vis = seen(w.req, (row0 + rows - 1) / a.n_heads);
-            // the two rows of this thread: how many keys they see
-            int lim[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = 16 * warp + g4 + 8 * h;
-                lim[h] = row < rows ? seen(w.req, (row0 + row) / a.n_heads) : 0;
-            }
-            float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, z[2] = {0.0f, 0.0f};
-            if (tid < rows)
-                s_out[tid] = (w.req.q0 + (row0 + tid) / a.n_heads) * a.ld_out_tok + (row0 + tid) % a.n_heads * a.ld_out_head;
-            if (vis > 0) {
-                // Q: 72 vectors of 16 bytes a row
-                for (int i = tid; i < nr * 72; i += kSoftThreads) {
-                    const int row = i / 72, v = i - row * 72;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const int tok = w.req.q0 + (row0 + row) / a.n_heads, head = (row0 + row) % a.n_heads;
-                        const uint16_t *src = v < 64 ? a.q_lat + tok * a.ld_qlat_tok + head * a.ld_qlat_head + 8 * v
-                                                     : a.q_rope + tok * a.ld_qrope_tok + head * a.ld_qrope_head + 8 * (v - 64);
-                        x = __ldg(reinterpret_cast<const uint4 *>(src));
-                    }
-                    *reinterpret_cast<uint4 *>(sm + lay.q + (v >> 3) * nr * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)) = x;
-                }
-                fence_async_shared();
-                bar_arrive(&b_q);
-                for (int t = 0; t < w.run; ++t, ++n) {
-                    const int j0 = (w.off + t) * kTile;
-                    wait(&b_s[n & 1], n >> 1);
-                    fence_after();
-                    float f[2] = {1.0f, 1.0f};
-                    float x[32];
-                    bool raise = false;
-                    if (active) {
-                        ld16x64(x, tm_s + lanes + uint32_t(n & 1) * kTile);
-                        wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (j0 + kTile > lim[h]) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (j0 + 8 * (i >> 1) + 2 * t4 + (i & 1) >= lim[h])
-                                        x[4 * (i >> 1) + 2 * h + (i & 1)] = -CUDART_INF_F;
-                            }
-                            float mx = x[2 * h];
-#pragma unroll
-                            for (int i = 1; i < 16; ++i)
-                                mx = fmaxf(mx, x[4 * (i >> 1) + 2 * h + (i & 1)]);
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                            mx *= sl;
-                            if (m[h] == -CUDART_INF_F) {
-                                m[h] = mx; // nothing summed yet
-                            } else if (mx > m[h] + kRaise) {
-                                f[h] = ex2(m[h] - mx);
-                                m[h] = mx;
-                                z[h] *= f[h];
-                                raise = true;
-                            }
-                            const float ref = m[h] == -CUDART_INF_F ? 0.0f : m[h];
-                            float sum = 0.0f;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float &e = x[4 * (i >> 1) + 2 * h + (i & 1)];
-                                e = ex2(fmaf(e, sl, -ref));
-                                sum += e;
-                            }
-                            z[h] += sum;
-                        }
-                    }
-                    // the last tile's second product has read P and written O
-                    if (t > 0)
-                        wait(&b_o, n - 1);
-                    if (active) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int row = 16 * warp + g4 + 8 * h;
-                            uint8_t *p = sm + lay.p + row * 128 + 4 * t4;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *reinterpret_cast<uint32_t *>(p + ((j ^ (row & 7)) << 4)) =
-                                    pack_bf16(x[4 * j + 2 * h], x[4 * j + 2 * h + 1]);
-                            if (t4 == 0)
-                                s_f[row] = f[h];
-                        }
-                    }
-                    if (j0 + kTile > vis) {
-                        // rows of the tile that nobody sees may hold anything: their weights are 0, 0 x NaN is not
-                        const int dead = kTile - (vis - j0), u0 = 4 * n;
-                        for (int i = tid; i < dead * 64; i += kSoftThreads) {
-                            const int c = i / (dead * 8), rest = i - c * dead * 8;
-                            const int k = (u0 + c / 2) % lay.units;
-                            *reinterpret_cast<uint4 *>(sm + lay.unit + k * kUnit + (c & 1) * kChunk + (vis - j0) * 128 +
-                                                       rest * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    if (sync_any(1, kSoftThreads, raise)) {
-                        fence_after();
-                        for (int c = 0; c < nr / 4; ++c) { // 16 columns: rows 16 c % nr .. of block 16 c / nr
-                            float o[16];
-                            ld32x16(o, tmem + lanes + uint32_t(16 * c));
-                            wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] *= s_f[(16 * c) % nr + i];
-                            st32x16(tmem + lanes + uint32_t(16 * c), o);
-                        }
-                        wait_st();
-                    }
-                    fence_before();
-                    fence_async_shared();
-                    bar_arrive(&b_p);
-                }
-                wait(&b_o, n - 1);
-                fence_after();
-            }
-            // ---- the run's result: the output, or a part of it ------------------------------
-            const bool whole = w.off == 0 && w.run == w.tiles;
-            const int slot = 2 * int(blockIdx.x) + (w.off == 0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                z[h] += __shfl_xor_sync(0xffffffffu, z[h], 1);
-                z[h] += __shfl_xor_sync(0xffffffffu, z[h], 2);
-                const int row = 16 * warp + g4 + 8 * h;
-                if (active && t4 == 0) {
-                    const float zi = z[h];
-                    s_z[row] = zi > 0.0f || zi != zi ? 1.0f / zi : 0.0f;
-                    if (row < rows) {
-                        if (!whole)
-                            parts.mz[slot * kMaxRows + row] = make_float2(m[h], zi);
-                        else if (a.lse)
-                            a.lse[int64_t(w.req.q0) * a.n_heads + row0 + row] =
-                                zi > 0.0f || zi != zi ? (m[h] + log2f(zi)) * kLn2 : -CUDART_INF_F;
-                    }
-                }
-            }
-            if (!whole && w.off > 0 && tid == 0) {
-                // the group runs over this CTA's start
-                const int64_t s0 = w.pos - w.off, s1 = s0 + w.tiles - 1; // the group's tiles in the line
-                Boundary b;
-                b.first = int(((s0 + 1) * ctas - 1) / total);
-                b.last = int(((s1 + 1) * ctas - 1) / total);
-                b.row0 = w.req.q0 * a.n_heads + row0;
-                b.rows = rows;
-                b.first_slot = 2 * b.first + 1;
-                parts.at[blockIdx.x] = b;
-            }
-            sync_some(1, kSoftThreads);
-            for (int c = 0; c < nr / 4; ++c) {
-                const int n0 = (16 * c) % nr, d0 = 128 * (16 * c / nr) + 32 * warp;
-                if (n0 >= rows)
-                    continue;
-                float o[16];
-                if (vis > 0) {
-                    ld32x16(o, tmem + lanes + uint32_t(16 * c));
-                    wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = 0.0f;
-                }
-                if (whole) {
-                    // lane pairs trade halves, so that each stores two columns of one row
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float e = o[i] * s_z[n0 + i], d = o[i + 1] * s_z[n0 + i + 1];
-                        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? e : d, 1);
-                        const int row = n0 + i + (lane & 1);
-                        if (row < rows)
-                            *reinterpret_cast<uint32_t *>(a.out + s_out[row] + d0 + (lane & ~1)) =
-                                lane & 1 ? pack_bf16(got, d) : pack_bf16(e, got);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (n0 + i < rows)
-                            parts.o[(size_t(slot) * kMaxRows + n0 + i) * W8_LATENT_DIM + d0 + lane] = o[i];
-                }
-            }
-            fence_before(); // the loads of O, before the next run's products
-            sync_some(1, kSoftThreads); // s_z is read
-        }
-    }
+    const int role = __shfl_sync(0xffffffffu, warp, 0);
+    auto roles = [&](auto rows) {
+        constexpr int NR = decltype(rows)::value;
+        return role == kCopyWarp    ? copy_role<NR>(a, map, w, sm, sh, lane)
+               : role == kScoreWarp ? score_role<NR>(a, w, sm, sh, tm_s)
+               : role == kOutWarp   ? out_role<NR>(a, w, sm, sh, tmem)
+                                    : softmax_role<NR>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid);
+    };
+    const bool ok = nr == 64   ? roles(std::integral_constant<int, 64>{})
+                    : nr == 32 ? roles(std::integral_constant<int, 32>{})
+                               : roles(std::integral_constant<int, 16>{});
     if (!ok)
         atomicOr(&g_paged_status, 1);
     pdl_launch_dependents();
