@@ -26,10 +26,9 @@
 // Seven warps: 0-3 softmax (16 rows each; loads S, writes P as bf16 into shared
 // memory, raises the reference, divides and stores), 4 copies (tensor-map
 // boxes of min(page, 64) tokens x 64 columns), 5 and 6 issue the two products
-// (a thread each: with one thread for both, a tile's second product waited
-// for the next tile's copies, 4.8 us a tile instead of XXX).  The ring
-// frees latent columns in units of 128 as the second product passes over
-// them; the rope chunk has a ring of its own and is free after the first.
+// (a warp each, so that a tile's second product does not wait for the next
+// tile's copies).  Two tiles are in flight, each in two halves: columns
+// 0 .. 255, freed when the second product has passed over them, and the rest.
 // The reference moves only when a row's maximum passes it by 2^8 (p stays
 // below 2^8, and 2^8 of fp32's range costs no precision): O is then rescaled
 // in tensor memory, for most inputs once or twice in the first tiles.
@@ -62,35 +61,36 @@ using namespace tcg;
 
 constexpr int kTile = 64;                    // tokens
 constexpr int kChunk = kTile * 128;          // bytes of 64 tokens x 64 columns
-constexpr int kUnit = 2 * kChunk;            // 128 latent columns
+constexpr int kFront = 4, kBack = 5;         // chunks of a tile's two halves: columns 0 .. 255, 256 .. 575
 constexpr int kMaxRows = 64;
 constexpr int kPagedThreads = 224, kSoftThreads = 128, kCopyWarp = 4, kScoreWarp = 5, kOutWarp = 6;
-constexpr int kMaxUnits = 12, kMaxRopes = 3;
+constexpr int kMaxSlots = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
 constexpr float kRaise = 8.0f;               // log2 of how far a row's weights may pass 1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Shared memory for groups of nr rows: Q, P, then the rings.
+// Shared memory for groups of nr rows: Q, P, then the two halves' rings.
 struct Smem {
-    int q, p, rope, unit, ropes, units;
+    int q, p, front, back, fronts, backs, end;
 };
 __host__ __device__ constexpr Smem smem_plan(int nr)
 {
     Smem s{};
     s.q = 0;
     s.p = s.q + 9 * nr * 128;
-    s.rope = s.p + nr * 128;
-    s.ropes = nr == 64 ? 2 : 3;
-    s.unit = s.rope + s.ropes * kChunk;
-    s.units = (kSmem - 1024 - s.unit) / kUnit;
-    s.units = s.units > kMaxUnits ? kMaxUnits : s.units;
+    s.front = s.p + nr * 128;
+    s.fronts = nr == 64 ? 2 : 3;
+    s.back = s.front + s.fronts * kFront * kChunk;
+    s.backs = 2;
+    s.end = s.back + s.backs * kBack * kChunk;
     return s;
 }
-static_assert(smem_plan(64).units >= 8 && smem_plan(32).units >= 8 && smem_plan(16).units >= 8, "two tiles in flight");
+static_assert(smem_plan(64).end <= kSmem - 1024 && smem_plan(32).end <= kSmem - 1024 && smem_plan(16).end <= kSmem - 1024,
+              "shared memory");
 // the first product reads 64 rows from every chunk of Q: the last chunk's
 // reach past Q stays inside the allocation
-static_assert(smem_plan(16).unit >= 8 * 16 * 128 + kChunk, "Q's reach");
+static_assert(smem_plan(16).end >= 8 * 16 * 128 + kChunk, "Q's reach");
 
 // What the parts of split groups need: [2 CTAs][64][512] fp32, [2 CTAs][64]
 // (m, z), [CTAs] the group that runs over the CTA's start.
@@ -177,12 +177,11 @@ struct Walk {
 
 // 2 KB at most: the rest is the rings'.
 struct Shared {
-    uint64_t unit_full[kMaxUnits], unit_free[kMaxUnits];
-    uint64_t rope_full[kMaxRopes], rope_free[kMaxRopes];
+    uint64_t front_full[kMaxSlots], front_free[kMaxSlots], back_full[kMaxSlots], back_free[kMaxSlots];
     uint64_t q, s[2], s_free[2], p, o, end[2];
     int64_t out[kMaxRows]; // a row's place in the output
     int64_t sum[kPagedThreads / 32];
-    int max[kPagedThreads / 32];
+    int max[kPagedThreads / 32], few[2][kPagedThreads / 32];
     int start[3];
     uint32_t tmem;
     float f[kMaxRows], inv[kMaxRows];
@@ -203,9 +202,7 @@ struct Turn {
     }
 };
 
-// One lane of a converged warp.  Tensor-core steps issued by a lane that the
-// compiler only knows as `lane == 0` take 85 to 130 cycles each whatever their
-// shape; issued under this they take their own 32 to 128.
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;
@@ -220,70 +217,90 @@ __device__ __forceinline__ int group_sees(const w8_latent_paged &a, const Walk &
 }
 
 // ---- copies ---------------------------------------------------------------
-template <int NR>
-__device__ __forceinline__ bool copy_role(const w8_latent_paged &a, const CUtensorMap &map, Walk w, uint8_t *sm, Shared &sh,
-                                          int lane)
+// One lane does it all: two waits, two byte counts and 9 BOXES copies a tile.
+// (The loop must be short: with four half-size units a tile, votes and a
+// shared loop body it took 2500 cycles a tile, near the tile's share of HBM.)
+template <int NR, int BOXES>
+__device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtensorMap &map, Walk w, uint8_t *sm, Shared &sh)
 {
     constexpr Smem lay = smem_plan(NR);
-    // lane l of a unit's copies: chunk l / boxes, box l % boxes
-    const int page = a.cache.page_size, box = min(page, kTile), boxes = kTile / box;
-    const int shift = 31 - __clz(page), bx = lane % boxes, c = lane / boxes;
-    Turn un, rn;
-    int units = 0, ropes = 0; // copied so far
+    constexpr int kBox = kTile / BOXES;
+    const int page = a.cache.page_size, shift = 31 - __clz(page);
+    const uint32_t front = smem_addr(sm + lay.front), back = smem_addr(sm + lay.back);
+    Turn f, b;
+    int tiles = 0; // copied so far
     bool ok = true;
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
         const int32_t *table = a.block_table + int64_t(w.r) * a.ld_table;
         const int vis = group_sees(a, w, NR);
-        // this lane's page of a tile; the next tile's is fetched ahead
-        auto page_of = [&](int t) {
-            const int j = t * kTile + bx * box;
-            int pg = a.cache.n_pages; // reads as zeros
-            if (t < w.off + w.run && j < vis) {
-                pg = __ldg(table + (j >> shift));
-                pg = pg < 0 || pg > a.cache.n_pages ? a.cache.n_pages : pg;
+        const int end = vis > 0 ? w.off + w.run : w.off; // a group that sees nothing has a tile of nothing
+        int pages[BOXES], ahead[BOXES]; // the next tile's pages are fetched ahead
+        auto fetch = [&](int (&pg)[BOXES], int t) {
+#pragma unroll
+            for (int i = 0; i < BOXES; ++i) {
+                const int j = t * kTile + i * kBox;
+                pg[i] = t < end && j < vis ? __ldg(table + (j >> shift)) : 0;
             }
-            return pg;
         };
-        int pg = page_of(w.off);
-        for (int t = w.off; ok && t < w.off + w.run; ++t) {
-            const int j0 = t * kTile, left = min(vis - j0, kTile);
-            if (left <= 0)
+        fetch(pages, w.off);
+        for (int t = w.off; t < end; ++t, ++tiles) {
+            fetch(ahead, t + 1);
+            const int left = min(vis - t * kTile, kTile);
+            const int need = (left + kBox - 1) / kBox;            // boxes with a key that is seen
+            const int y = BOXES == 1 ? t * kTile & (page - 1) : 0; // a page of several tiles
+#pragma unroll
+            for (int i = 0; i < BOXES; ++i) // a number that is no page reads as zeros
+                pages[i] = pages[i] < 0 || pages[i] > a.cache.n_pages ? a.cache.n_pages : pages[i];
+            if (tiles >= lay.fronts)
+                ok = bar_wait(&sh.front_free[f.k], f.parity ^ 1);
+            if (!ok)
                 break;
-            const int need = (left + box - 1) / box; // boxes with a key that is seen
-            const int y = (j0 + bx * box) & (page - 1);
-            const int ahead = page_of(t + 1);
-            for (int u = 0; u < 5; ++u) {
-                const bool rope = u == 4;
-                const int k = rope ? rn.k : un.k;
-                uint64_t *full = rope ? &sh.rope_full[k] : &sh.unit_full[k];
-                if (rope ? ropes >= lay.ropes : units >= lay.units)
-                    ok = __all_sync(0xffffffffu, rope ? bar_wait(&sh.rope_free[k], rn.parity ^ 1)
-                                                      : bar_wait(&sh.unit_free[k], un.parity ^ 1));
-                if (!ok)
-                    break;
-                const int chunks = rope ? 1 : 2;
-                if (lane == 0)
-                    bar_expect(full, uint32_t(chunks * need * box * 128));
-                __syncwarp();
-                if (c < chunks && bx < need)
-                    copy_box(smem_addr(sm + (rope ? lay.rope + k * kChunk : lay.unit + k * kUnit) + c * kChunk + bx * box * 128),
-                             &map, 64 * (2 * u + c), y, pg, full);
-                if (rope) {
-                    rn.step(lay.ropes);
-                    ++ropes;
-                } else {
-                    un.step(lay.units);
-                    ++units;
-                }
-            }
-            pg = ahead;
+            bar_expect(&sh.front_full[f.k], uint32_t(kFront * kBox * 128) * need);
+#pragma unroll
+            for (int c = 0; c < kFront; ++c)
+#pragma unroll
+                for (int i = 0; i < BOXES; ++i)
+                    if (i < need)
+                        copy_box(front + uint32_t(f.k * kFront * kChunk + c * kChunk + i * kBox * 128), &map, 64 * c, y, pages[i],
+                                 &sh.front_full[f.k]);
+            f.step(lay.fronts);
+            if (tiles >= lay.backs)
+                ok = bar_wait(&sh.back_free[b.k], b.parity ^ 1);
+            if (!ok)
+                break;
+            bar_expect(&sh.back_full[b.k], uint32_t(kBack * kBox * 128) * need);
+#pragma unroll
+            for (int c = 0; c < kBack; ++c)
+#pragma unroll
+                for (int i = 0; i < BOXES; ++i)
+                    if (i < need)
+                        copy_box(back + uint32_t(b.k * kBack * kChunk + c * kChunk + i * kBox * 128), &map, 64 * (kFront + c), y,
+                                 pages[i], &sh.back_full[b.k]);
+            b.step(lay.backs);
+#pragma unroll
+            for (int i = 0; i < BOXES; ++i)
+                pages[i] = ahead[i];
         }
     }
     // the copies still in flight (there are any only after a wait elsewhere gave up)
-    for (int i = max(0, units - lay.units); i < units; ++i)
-        bar_wait(&sh.unit_full[i % lay.units], uint32_t((i / lay.units) & 1));
-    for (int i = max(0, ropes - lay.ropes); i < ropes; ++i)
-        bar_wait(&sh.rope_full[i % lay.ropes], uint32_t((i / lay.ropes) & 1));
+    if (!ok)
+        ++tiles; // a front half may be on its way without its back half
+    for (int i = max(0, tiles - lay.fronts); i < tiles; ++i)
+        bar_wait(&sh.front_full[i % lay.fronts], uint32_t((i / lay.fronts) & 1));
+    for (int i = max(0, tiles - lay.backs); i < tiles; ++i)
+        bar_wait(&sh.back_full[i % lay.backs], uint32_t((i / lay.backs) & 1));
+    return ok;
+}
+template <int NR>
+__device__ __forceinline__ bool copy_role(const w8_latent_paged &a, const CUtensorMap &map, const Walk &w, uint8_t *sm, Shared &sh)
+{
+    bool ok = true;
+    if (elect_one()) {
+        ok = a.cache.page_size == 16   ? copy_loop<NR, 4>(a, map, w, sm, sh)
+             : a.cache.page_size == 32 ? copy_loop<NR, 2>(a, map, w, sm, sh)
+                                       : copy_loop<NR, 1>(a, map, w, sm, sh);
+    }
+    __syncwarp();
     return ok;
 }
 
@@ -294,9 +311,9 @@ __device__ __forceinline__ bool score_role(const w8_latent_paged &a, Walk w, uin
     constexpr Smem lay = smem_plan(NR);
     constexpr uint32_t id = inst_desc(64, kTile, false, false);
     const uint64_t dq = desc128_k(smem_addr(sm + lay.q), 1024);
-    const uint64_t drope = desc128_k(smem_addr(sm + lay.rope), 1024), dunit = desc128_k(smem_addr(sm + lay.unit), 1024);
+    const uint64_t dfront = desc128_k(smem_addr(sm + lay.front), 1024), dback = desc128_k(smem_addr(sm + lay.back), 1024);
     const bool one = elect_one();
-    Turn un, rn;
+    Turn f, b;
     int runs = 0, n = 0; // runs with keys, tiles
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, parity & 1)); };
@@ -310,36 +327,33 @@ __device__ __forceinline__ bool score_role(const w8_latent_paged &a, Walk w, uin
             if (n >= 2)
                 wait(&sh.s_free[n & 1], uint32_t(n / 2 - 1));
             const uint32_t d = tm_s + uint32_t(n & 1) * kTile;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                wait(&sh.unit_full[un.k], un.parity);
-                if (!ok)
-                    break;
-                fence_after();
-                const uint64_t dk = dunit + uint64_t((un.k * kUnit) >> 4);
-                if (one) {
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ss(d, dq + uint64_t(((2 * u + s / 4) * NR * 128 + (s % 4) * 32) >> 4),
-                               dk + uint64_t(((s / 4) * kChunk + (s % 4) * 32) >> 4), id, uint32_t(u | s));
-                }
-                __syncwarp();
-                un.step(lay.units);
-            }
-            wait(&sh.rope_full[rn.k], rn.parity);
+            wait(&sh.front_full[f.k], f.parity);
             if (!ok)
                 break;
             fence_after();
-            const uint64_t dk = drope + uint64_t((rn.k * kChunk) >> 4);
+            const uint64_t df = dfront + uint64_t((f.k * kFront * kChunk) >> 4);
             if (one) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    mma_ss(d, dq + uint64_t((8 * NR * 128 + s * 32) >> 4), dk + uint64_t((s * 32) >> 4), id, 1);
-                commit(&sh.rope_free[rn.k]);
+                for (int s = 0; s < 4 * kFront; ++s)
+                    mma_ss(d, dq + uint64_t(((s / 4) * NR * 128 + (s % 4) * 32) >> 4),
+                           df + uint64_t(((s / 4) * kChunk + (s % 4) * 32) >> 4), id, uint32_t(s));
+            }
+            __syncwarp();
+            f.step(lay.fronts);
+            wait(&sh.back_full[b.k], b.parity);
+            if (!ok)
+                break;
+            fence_after();
+            const uint64_t db = dback + uint64_t((b.k * kBack * kChunk) >> 4);
+            if (one) {
+#pragma unroll
+                for (int s = 0; s < 4 * kBack; ++s)
+                    mma_ss(d, dq + uint64_t(((kFront + s / 4) * NR * 128 + (s % 4) * 32) >> 4),
+                           db + uint64_t(((s / 4) * kChunk + (s % 4) * 32) >> 4), id, 1);
                 commit(&sh.s[n & 1]);
             }
             __syncwarp();
-            rn.step(lay.ropes);
+            b.step(lay.backs);
         }
     }
     // nothing of this warp's is in the tensor cores when the CTA frees its memory
@@ -355,9 +369,10 @@ __device__ __forceinline__ bool out_role(const w8_latent_paged &a, Walk w, uint8
 {
     constexpr Smem lay = smem_plan(NR);
     constexpr uint32_t id = inst_desc(128, NR, true, false);
-    const uint64_t dp = desc128_k(smem_addr(sm + lay.p), 1024), dunit = desc128(smem_addr(sm + lay.unit), kChunk, 1024);
+    const uint64_t dp = desc128_k(smem_addr(sm + lay.p), 1024), dfront = desc128(smem_addr(sm + lay.front), kChunk, 1024),
+                   dback = desc128(smem_addr(sm + lay.back), kChunk, 1024);
     const bool one = elect_one();
-    Turn un;
+    Turn f, b;
     int n = 0;
     bool ok = true;
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
@@ -368,22 +383,23 @@ __device__ __forceinline__ bool out_role(const w8_latent_paged &a, Walk w, uint8
             if (!ok)
                 break;
             fence_after();
+            const uint64_t df = dfront + uint64_t((f.k * kFront * kChunk) >> 4), db = dback + uint64_t((b.k * kBack * kChunk) >> 4);
+            if (one) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint64_t dv = dunit + uint64_t((un.k * kUnit) >> 4);
-                if (one) {
+                for (int u = 0; u < 4; ++u) {
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_ss(tmem + uint32_t(u * NR), dv + uint64_t((s * 2048) >> 4), dp + uint64_t((s * 32) >> 4), id,
-                               uint32_t(t | s));
-                    commit(&sh.unit_free[un.k]);
+                        mma_ss(tmem + uint32_t(u * NR), (u < 2 ? df : db) + uint64_t(((u % 2) * 2 * kChunk + s * 2048) >> 4),
+                               dp + uint64_t((s * 32) >> 4), id, uint32_t(t | s));
+                    if (u == 1)
+                        commit(&sh.front_free[f.k]);
                 }
-                __syncwarp();
-                un.step(lay.units);
-            }
-            if (one)
+                commit(&sh.back_free[b.k]);
                 commit(&sh.o);
+            }
             __syncwarp();
+            f.step(lay.fronts);
+            b.step(lay.backs);
         }
     }
     if (one)
@@ -431,26 +447,17 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
         }
         sync_some(1, kSoftThreads);
         if (vis > 0) {
-            // Q: 72 vectors of 16 bytes a row, nine loads of a thread in flight
-            constexpr int kBatch = 9;
-#pragma unroll 1
-            for (int i0 = 0; i0 < NR * 72; i0 += kBatch * kSoftThreads) {
-                uint4 x[kBatch];
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int i = i0 + b * kSoftThreads + tid, row = i / 72, v = i - row * 72;
-                    x[b] = make_uint4(0, 0, 0, 0);
-                    if (row < rows)
-                        x[b] = __ldg(reinterpret_cast<const uint4 *>(v < 64 ? a.q_lat + q_at[row] + 8 * v
-                                                                            : a.q_rope + q_at[NR + row] + 8 * (v - 64)));
-                }
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int i = i0 + b * kSoftThreads + tid, row = i / 72, v = i - row * 72;
-                    *reinterpret_cast<uint4 *>(sm + lay.q + (v >> 3) * NR * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)) =
-                        x[b];
-                }
+            // Q: 72 vectors of 16 bytes a row, all in flight at once; rows past the group's are zeros
+#pragma unroll 4
+            for (int i = tid; i < NR * 72; i += kSoftThreads) {
+                const int row = i / 72, v = i - row * 72;
+                const uint16_t *src = a.q_lat;
+                if (row < rows)
+                    src = v < 64 ? a.q_lat + q_at[row] + 8 * v : a.q_rope + q_at[NR + row] + 8 * (v - 64);
+                copy16(smem_addr(sm + lay.q) + uint32_t((v >> 3) * NR * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)), src,
+                       row < rows);
             }
+            copy16_wait();
             fence_async_shared();
             bar_arrive(&sh.q);
             for (int t = 0; t < w.run; ++t, ++n) {
@@ -475,10 +482,12 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                                 if (j0 + 8 * (i >> 1) + 2 * t4 + (i & 1) >= lim[h])
                                     x[4 * (i >> 1) + 2 * h + (i & 1)] = -CUDART_INF_F;
                         }
-                        float mx = x[2 * h];
+                        float top[8];
 #pragma unroll
-                        for (int i = 1; i < 16; ++i)
-                            mx = fmaxf(mx, x[4 * (i >> 1) + 2 * h + (i & 1)]);
+                        for (int i = 0; i < 8; ++i)
+                            top[i] = fmaxf(x[4 * i + 2 * h], x[4 * i + 2 * h + 1]);
+                        float mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
+                                         fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         mx *= sl;
@@ -491,14 +500,14 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                             raise = true;
                         }
                         const float ref = m[h] == -CUDART_INF_F ? 0.0f : m[h];
-                        float sum = 0.0f;
+                        float sum[4] = {};
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float &e = x[4 * (i >> 1) + 2 * h + (i & 1)];
                             e = ex2(fmaf(e, sl, -ref));
-                            sum += e;
+                            sum[i & 3] += e;
                         }
-                        z[h] += sum;
+                        z[h] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     }
                 }
                 // the last tile's second product has read P and written O
@@ -522,9 +531,9 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                     const int dead = kTile - (vis - j0);
                     for (int i = tid; i < dead * 64; i += kSoftThreads) {
                         const int c = i / (dead * 8), rest = i - c * dead * 8;
-                        const int k = (4 * n + c / 2) % lay.units;
-                        *reinterpret_cast<uint4 *>(sm + lay.unit + k * kUnit + (c & 1) * kChunk + (vis - j0) * 128 +
-                                                   rest * 16) = make_uint4(0, 0, 0, 0);
+                        uint8_t *half = c < kFront ? sm + lay.front + (n % lay.fronts * kFront + c) * kChunk
+                                                   : sm + lay.back + (n % lay.backs * kBack + c - kFront) * kChunk;
+                        *reinterpret_cast<uint4 *>(half + (vis - j0) * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 if (sync_any(1, kSoftThreads, raise)) {
@@ -626,13 +635,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *const sm = s_dyn + ((1024u - (smem_addr(s_dyn) & 1023u)) & 1023u);
     if (tid == 0) {
-        for (int i = 0; i < kMaxUnits; ++i) {
-            bar_init(&sh.unit_full[i], 1);
-            bar_init(&sh.unit_free[i], 1);
-        }
-        for (int i = 0; i < kMaxRopes; ++i) {
-            bar_init(&sh.rope_full[i], 1);
-            bar_init(&sh.rope_free[i], 1);
+        for (int i = 0; i < kMaxSlots; ++i) {
+            bar_init(&sh.front_full[i], 1);
+            bar_init(&sh.front_free[i], 1);
+            bar_init(&sh.back_full[i], 1);
+            bar_init(&sh.back_free[i], 1);
         }
         bar_init(&sh.q, kSoftThreads);
         bar_init(&sh.s[0], 1);
@@ -649,48 +656,59 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         tmem_alloc(&sh.tmem, kTmemCols);
     pdl_wait();
 
-    // ---- the line of tiles: its length, NR, this CTA's run -------------------
+    // ---- the line of tiles: NR, its length, this CTA's run -------------------
     const int per = (a.n_req + kPagedThreads - 1) / kPagedThreads;
     const int r0 = min(tid * per, a.n_req), r1 = min(r0 + per, a.n_req);
-    int nr = kMaxRows;
-    int64_t mine = 0, before = 0, total = 0;
-    for (;;) {
-        mine = 0;
-        int rows = 0;
+    Request held{0, 0, 0}; // the thread's first request, mostly its only one
+    if (r0 < r1)
+        held = request_of(a, r0);
+    // this thread's tiles with nr rows a group
+    auto tiles_of = [&](int nr) {
+        int64_t sum = 0;
         for (int r = r0; r < r1; ++r) {
-            const Request q = request_of(a, r);
-            rows = max(rows, min(q.q * a.n_heads, kMaxRows));
+            const Request q = r == r0 ? held : request_of(a, r);
             const int n = groups_of(q, a.n_heads, nr);
             for (int g = 0; g < n; ++g)
-                mine += group_tiles(q, a.n_heads, nr, g);
+                sum += group_tiles(q, a.n_heads, nr, g);
         }
-        int64_t inc = mine;
+        return sum;
+    };
+    int rows = 0;
+    for (int r = r0; r < r1; ++r)
+        rows = max(rows, min((r == r0 ? held : request_of(a, r)).q * a.n_heads, kMaxRows));
+    // fewer rows a group: when no group would be filled, or when twice as many
+    // groups still leave no SM two tiles (a count past 2^16 is many)
+    rows = __reduce_max_sync(0xffffffffu, rows);
+    const int n64 = __reduce_add_sync(0xffffffffu, int(min(tiles_of(64), int64_t(1 << 16))));
+    const int n32 = __reduce_add_sync(0xffffffffu, int(min(tiles_of(32), int64_t(1 << 16))));
+    if (lane == 0) {
+        sh.max[warp] = rows;
+        sh.few[0][warp] = n64;
+        sh.few[1][warp] = n32;
+    }
+    __syncthreads();
+    int all64 = 0, all32 = 0;
+    for (int i = 0; i < kPagedThreads / 32; ++i) {
+        rows = max(rows, sh.max[i]);
+        all64 += sh.few[0][i];
+        all32 += sh.few[1][i];
+    }
+    const int grid = int(gridDim.x);
+    const int nr = rows > 32 && all64 * 2 > grid ? 64 : rows > 16 && all32 * 2 > grid ? 32 : 16;
+    const int64_t mine = tiles_of(nr);
+    int64_t inc = mine;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
-            inc += lane >= d ? o : 0;
-            rows = max(rows, __shfl_xor_sync(0xffffffffu, rows, d));
-        }
-        __syncthreads(); // the last pass's sums are read
-        if (lane == 31) {
-            sh.sum[warp] = inc;
-            sh.max[warp] = rows;
-        }
-        __syncthreads();
-        before = inc - mine;
-        total = 0;
-        rows = 0;
-        for (int w = 0; w < kPagedThreads / 32; ++w) {
-            before += w < warp ? sh.sum[w] : 0;
-            total += sh.sum[w];
-            rows = max(rows, sh.max[w]);
-        }
-        // fewer rows a group: when no group would be filled, or when that
-        // many more groups still leave no SM two tiles
-        const int half = nr / 2;
-        if (nr == 16 || !(rows <= half || total * 2 <= gridDim.x))
-            break;
-        nr = half;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+        inc += lane >= d ? o : 0;
+    }
+    if (lane == 31)
+        sh.sum[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - mine, total = 0;
+    for (int i = 0; i < kPagedThreads / 32; ++i) {
+        before += i < warp ? sh.sum[i] : 0;
+        total += sh.sum[i];
     }
     const int64_t ctas = min(total, int64_t(gridDim.x)); // those that have work
     Walk w{};
@@ -699,7 +717,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
         int64_t at = before;
         for (int r = r0; r < r1; ++r) {
-            const Request q = request_of(a, r);
+            const Request q = r == r0 ? held : request_of(a, r);
             const int n = groups_of(q, a.n_heads, nr);
             for (int g = 0; g < n; ++g) {
                 const int t = group_tiles(q, a.n_heads, nr, g);
@@ -723,7 +741,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const int role = __shfl_sync(0xffffffffu, warp, 0);
     auto roles = [&](auto rows) {
         constexpr int NR = decltype(rows)::value;
-        return role == kCopyWarp    ? copy_role<NR>(a, map, w, sm, sh, lane)
+        return role == kCopyWarp    ? copy_role<NR>(a, map, w, sm, sh)
                : role == kScoreWarp ? score_role<NR>(a, w, sm, sh, tm_s)
                : role == kOutWarp   ? out_role<NR>(a, w, sm, sh, tmem)
                                     : softmax_role<NR>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid);
@@ -742,66 +760,89 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     }
 }
 
-// Joins the parts of a split group: a block a (CTA start, row), a thread four
-// latent columns.  The block of the group's first crossed start does it.
-__global__ void __launch_bounds__(W8_LATENT_DIM / 4)
+// Joins the parts of the split groups: a block takes one row of one group at
+// a time, a thread four latent columns.  The crossed CTA starts are listed in
+// shared memory first; a group is named by the first start that it crosses.
+constexpr int kJoinThreads = W8_LATENT_DIM / 4, kMaxCtas = 1024;
+__global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const __grid_constant__ w8_latent_paged a, void *ws, int ctas)
 {
-    __shared__ float s_w[1024];
-    __shared__ float s_m[4], s_z[4];
-    const int tid = threadIdx.x, cta = blockIdx.x + 1, row = blockIdx.y;
+    __shared__ int s_list[kMaxCtas];
+    __shared__ int s_n;
+    __shared__ uint8_t s_yes[kMaxCtas];
+    const int tid = threadIdx.x;
     pdl_wait();
     const Parts parts = parts_of(ws, ctas);
-    const Boundary b = parts.at[cta];
-    if (b.last < 0 || b.first != cta - 1 || row >= b.rows)
-        return;
-    const int n = b.last - b.first + 1;
-    // part i: the first CTA's, then slot 2 c of each later one
-    auto slot = [&](int i) { return size_t(i ? 2 * (b.first + i) : b.first_slot) * kMaxRows + row; };
-    // the weights 2^(m_i - m): one pass for m, one for the sum
-    float m = -CUDART_INF_F;
-    for (int i = tid; i < n; i += blockDim.x)
-        m = fmaxf(m, parts.mz[slot(i)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((tid & 31) == 0)
-        s_m[tid >> 5] = m;
+    for (int c = 1 + tid; c < ctas; c += kJoinThreads)
+        s_yes[c] = parts.at[c].last >= 0 && parts.at[c].first == c - 1;
     __syncthreads();
-    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    const float ref = m == -CUDART_INF_F ? 0.0f : m;
-    float z = 0.0f;
-    for (int i = tid; i < n; i += blockDim.x) {
-        const float2 mz = parts.mz[slot(i)];
-        const float f = mz.x == -CUDART_INF_F ? 0.0f : ex2(mz.x - ref); // nothing seen: O is 0
-        s_w[i] = f;
-        z += mz.y * f;
+    if (tid < 32) { // in order: every block has the same list
+        int n = 0;
+        for (int c0 = 1; c0 < ctas; c0 += 32) {
+            const int c = c0 + tid;
+            const bool yes = c < ctas && s_yes[c] != 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, yes);
+            if (yes)
+                s_list[n + __popc(all & ((1u << tid) - 1))] = c;
+            n += __popc(all);
+        }
+        if (tid == 0)
+            s_n = n;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        z += __shfl_xor_sync(0xffffffffu, z, d);
-    if ((tid & 31) == 0)
-        s_z[tid >> 5] = z;
     __syncthreads();
-    z = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float4 v = reinterpret_cast<const float4 *>(parts.o + slot(i) * W8_LATENT_DIM)[tid];
-        const float f = s_w[i];
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
+    for (int job = blockIdx.x; job < s_n * kMaxRows; job += gridDim.x) {
+        const Boundary b = parts.at[s_list[job % s_n]];
+        const int row = job / s_n, n = b.last - b.first + 1;
+        if (row >= b.rows)
+            continue;
+        // part i: the first CTA's, then slot 2 c of each later one; eight
+        // parts' loads are in flight at once, and no thread waits for another
+        auto slot = [&](int i) { return size_t(i ? 2 * (b.first + i) : b.first_slot) * kMaxRows + row; };
+        float m = -CUDART_INF_F, z = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float2 mz[8];
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                mz[i] = make_float2(-CUDART_INF_F, 0.0f);
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < n) {
+                    mz[i] = parts.mz[slot(i0 + i)];
+                    v[i] = reinterpret_cast<const float4 *>(parts.o + slot(i0 + i) * W8_LATENT_DIM)[tid];
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                top = fmaxf(top, mz[i].x);
+            const float ref = top == -CUDART_INF_F ? 0.0f : top;
+            const float f0 = ex2(m - ref);
+            m = top;
+            z *= f0;
+            o.x *= f0;
+            o.y *= f0;
+            o.z *= f0;
+            o.w *= f0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = ex2(mz[i].x - ref); // 0 for a part that has seen nothing (its O is 0)
+                z = fmaf(mz[i].y, f, z);
+                o.x = fmaf(v[i].x, f, o.x);
+                o.y = fmaf(v[i].y, f, o.y);
+                o.z = fmaf(v[i].z, f, o.z);
+                o.w = fmaf(v[i].w, f, o.w);
+            }
+        }
+        const bool some = z > 0.0f || z != z;
+        const float inv = some ? 1.0f / z : 0.0f;
+        const int tok = (b.row0 + row) / a.n_heads, head = (b.row0 + row) % a.n_heads;
+        uint32_t *out = reinterpret_cast<uint32_t *>(a.out + tok * a.ld_out_tok + head * a.ld_out_head) + 2 * tid;
+        out[0] = pack_bf16(o.x * inv, o.y * inv);
+        out[1] = pack_bf16(o.z * inv, o.w * inv);
+        if (a.lse && tid == 0)
+            a.lse[b.row0 + row] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
     }
-    const bool some = z > 0.0f || z != z;
-    const float inv = some ? 1.0f / z : 0.0f;
-    const int tok = (b.row0 + row) / a.n_heads, head = (b.row0 + row) % a.n_heads;
-    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + tok * a.ld_out_tok + head * a.ld_out_head) + 2 * tid;
-    out[0] = pack_bf16(o.x * inv, o.y * inv);
-    out[1] = pack_bf16(o.z * inv, o.w * inv);
-    if (a.lse && tid == 0)
-        a.lse[b.row0 + row] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
@@ -844,6 +885,8 @@ size_t latent_paged_ws_bytes(int, int, int, int sms) { return parts_bytes(sms); 
 
 cudaError_t launch_latent_paged(const w8_latent_paged &a, void *ws, int sms, cudaStream_t s)
 {
+    if (sms > kMaxCtas)
+        return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&paged_kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess)
@@ -857,9 +900,7 @@ cudaError_t launch_latent_paged(const w8_latent_paged &a, void *ws, int sms, cud
     e = launch_dependent(&paged_kernel, dim3(unsigned(sms)), kPagedThreads, kSmem, s, a, map, ws);
     if (e != cudaSuccess || sms < 2)
         return e;
-    const int64_t rows = int64_t(a.n_tok) * a.n_heads;
-    return launch_dependent(&join_kernel, dim3(unsigned(sms - 1), unsigned(rows < kMaxRows ? rows : kMaxRows)),
-                            W8_LATENT_DIM / 4, 0, s, a, ws, sms);
+    return launch_dependent(&join_kernel, dim3(unsigned(12 * sms)), kJoinThreads, 0, s, a, ws, sms);
 }
 
 cudaError_t paged_status(int *out, bool reset)

@@ -91,6 +91,13 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, i
                  : "memory");
 }
 
+// 16 bytes global -> shared (zeros when !some; src is then not read), asynchronously.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Shared-memory matrix descriptor, 128-byte swizzle (atoms of 8 rows of 128
 // bytes, 1024-byte aligned).  K-major operand (a row = 64 values along K):
 // sbo = bytes between 8-row atoms, lbo unused (1).  MN-major operand (a row =
