@@ -63,7 +63,7 @@ constexpr int kTile = 64;                    // tokens
 constexpr int kChunk = kTile * 128;          // bytes of 64 tokens x 64 columns
 constexpr int kFront = 4, kBack = 5;         // chunks of a tile's two halves: columns 0 .. 255, 256 .. 575
 constexpr int kMaxRows = 64;
-constexpr int kPagedThreads = 224, kSoftThreads = 128, kCopyWarp = 4, kScoreWarp = 5, kOutWarp = 6;
+constexpr int kPagedThreads = 352, kSoftThreads = 256, kCopyWarp = 8, kScoreWarp = 9, kOutWarp = 10;
 constexpr int kMaxSlots = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
@@ -184,7 +184,7 @@ struct Shared {
     int max[kPagedThreads / 32], few[2][kPagedThreads / 32];
     int start[3];
     uint32_t tmem;
-    float f[kMaxRows], inv[kMaxRows];
+    float f[kMaxRows], top[2][kMaxRows];
 };
 
 static_assert(sizeof(Shared) <= 227 * 1024 - kSmem, "shared memory");
@@ -221,7 +221,7 @@ __device__ __forceinline__ int group_sees(const w8_latent_paged &a, const Walk &
 // (The loop must be short: with four half-size units a tile, votes and a
 // shared loop body it took 2500 cycles a tile, near the tile's share of HBM.)
 template <int NR, int BOXES>
-__device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtensorMap &map, Walk w, uint8_t *sm, Shared &sh)
+__device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtensorMap &map, Walk w, uint8_t *sm, Shared &sh, uint64_t policy)
 {
     constexpr Smem lay = smem_plan(NR);
     constexpr int kBox = kTile / BOXES;
@@ -262,7 +262,7 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
                 for (int i = 0; i < BOXES; ++i)
                     if (i < need)
                         copy_box(front + uint32_t(f.k * kFront * kChunk + c * kChunk + i * kBox * 128), &map, 64 * c, y, pages[i],
-                                 &sh.front_full[f.k]);
+                                 &sh.front_full[f.k], policy);
             f.step(lay.fronts);
             if (tiles >= lay.backs)
                 ok = bar_wait(&sh.back_free[b.k], b.parity ^ 1);
@@ -275,7 +275,7 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
                 for (int i = 0; i < BOXES; ++i)
                     if (i < need)
                         copy_box(back + uint32_t(b.k * kBack * kChunk + c * kChunk + i * kBox * 128), &map, 64 * (kFront + c), y,
-                                 pages[i], &sh.back_full[b.k]);
+                                 pages[i], &sh.back_full[b.k], policy);
             b.step(lay.backs);
 #pragma unroll
             for (int i = 0; i < BOXES; ++i)
@@ -292,13 +292,15 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
     return ok;
 }
 template <int NR>
-__device__ __forceinline__ bool copy_role(const w8_latent_paged &a, const CUtensorMap &map, const Walk &w, uint8_t *sm, Shared &sh)
+__device__ __forceinline__ bool copy_role(const w8_latent_paged &a, const CUtensorMap &map, const Walk &w, uint8_t *sm, Shared &sh, bool once)
 {
     bool ok = true;
     if (elect_one()) {
-        ok = a.cache.page_size == 16   ? copy_loop<NR, 4>(a, map, w, sm, sh)
-             : a.cache.page_size == 32 ? copy_loop<NR, 2>(a, map, w, sm, sh)
-                                       : copy_loop<NR, 1>(a, map, w, sm, sh);
+        // rows that one group reads leave L2 first: the parts of split groups stay
+        const uint64_t policy = once ? policy_first() : policy_normal();
+        ok = a.cache.page_size == 16   ? copy_loop<NR, 4>(a, map, w, sm, sh, policy)
+             : a.cache.page_size == 32 ? copy_loop<NR, 2>(a, map, w, sm, sh, policy)
+                                       : copy_loop<NR, 1>(a, map, w, sm, sh, policy);
     }
     __syncwarp();
     return ok;
@@ -409,153 +411,203 @@ __device__ __forceinline__ bool out_role(const w8_latent_paged &a, Walk w, uint8
 }
 
 // ---- softmax, output --------------------------------------------------------
+// Q of the walk's run, all copies in flight at once: a warp a row, 72 vectors
+// of 16 bytes; rows past the group's are zeros.
+template <int NR>
+__device__ __forceinline__ void load_q(const w8_latent_paged &a, const Walk &w, uint8_t *q, int warp, int lane)
+{
+    const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
+#pragma unroll 2
+    for (int row = warp; row < NR; row += kSoftThreads / 32) {
+        const bool some = row < rows;
+        const int tok = some ? (row0 + row) / a.n_heads : 0, head = some ? row0 + row - tok * a.n_heads : 0;
+        const uint16_t *lat = a.q_lat + (w.req.q0 + tok) * a.ld_qlat_tok + head * a.ld_qlat_head;
+        const uint16_t *rope = a.q_rope + (w.req.q0 + tok) * a.ld_qrope_tok + head * a.ld_qrope_head;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int v = 32 * k + lane;
+            if (v < 72)
+                copy16(smem_addr(q + (v >> 3) * NR * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)),
+                       v < 64 ? lat + 8 * v : rope + 8 * (v - 64), some);
+        }
+    }
+}
+
 template <int NR>
 __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, uint32_t tmem,
                                              uint32_t tm_s, const Parts &parts, int64_t total, int64_t ctas, int tid)
 {
     constexpr Smem lay = smem_plan(NR);
     const int warp = tid >> 5, lane = tid & 31;
+    // warps w and w + 4 share 16 rows: tokens 0 .. 31 and 32 .. 63 of the tile
+    const int quarter = warp & 3, half = warp >> 2;
     const float sl = a.scale * kLog2e;
     const int g4 = lane >> 2, t4 = lane & 3;
-    const bool active = 16 * warp < NR; // warps that have rows
-    const uint32_t lanes = uint32_t(32 * warp) << 16;
+    const bool active = 16 * quarter < NR; // warps that have rows
+    const uint32_t lanes = uint32_t(32 * quarter) << 16;
+    const int row_h[2] = {16 * quarter + g4, 16 * quarter + g4 + 8}; // this thread's rows
     bool ok = true;
     // a wait that gave up is followed by no other, but every barrier below is
     // still met, so that no warp waits for one that left
     auto wait = [&](uint64_t *bar, int phase) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, uint32_t(phase & 1))); };
     if (tid == 0 && (w.pos >= w.end || w.off == 0))
         parts.at[blockIdx.x].last = -1; // no group runs over this CTA's start
-    // the rows' places in Q, while Q is loaded, where P will be
-    int64_t *const q_at = reinterpret_cast<int64_t *>(sm + lay.p);
     int n = 0; // tiles so far
-    for (bool first = true; w.next(a, NR, first); first = false) {
+    bool loaded = false;
+    for (bool have = w.next(a, NR, true); have;) {
         const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
         const int vis = seen(w.req, (row0 + rows - 1) / a.n_heads);
-        // the two rows of this thread: how many keys they see
-        int lim[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = 16 * warp + g4 + 8 * h;
-            lim[h] = row < rows ? seen(w.req, (row0 + row) / a.n_heads) : 0;
-        }
-        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, z[2] = {0.0f, 0.0f};
-        if (tid < rows) {
-            const int tok = w.req.q0 + (row0 + tid) / a.n_heads, head = (row0 + tid) % a.n_heads;
-            sh.out[tid] = tok * a.ld_out_tok + head * a.ld_out_head;
-            q_at[tid] = tok * a.ld_qlat_tok + head * a.ld_qlat_head;
-            q_at[NR + tid] = tok * a.ld_qrope_tok + head * a.ld_qrope_head;
-        }
-        sync_some(1, kSoftThreads);
-        if (vis > 0) {
-            // Q: 72 vectors of 16 bytes a row, all in flight at once; rows past the group's are zeros
-#pragma unroll 4
-            for (int i = tid; i < NR * 72; i += kSoftThreads) {
-                const int row = i / 72, v = i - row * 72;
-                const uint16_t *src = a.q_lat;
-                if (row < rows)
-                    src = v < 64 ? a.q_lat + q_at[row] + 8 * v : a.q_rope + q_at[NR + row] + 8 * (v - 64);
-                copy16(smem_addr(sm + lay.q) + uint32_t((v >> 3) * NR * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)), src,
-                       row < rows);
-            }
+        if (vis > 0 && !loaded) {
+            load_q<NR>(a, w, sm + lay.q, warp, lane);
             copy16_wait();
             fence_async_shared();
             bar_arrive(&sh.q);
+        }
+        loaded = false;
+        Walk nx = w;
+        const bool more = nx.next(a, NR, false);
+        const bool ahead = more && group_sees(a, nx, NR) > 0; // the next run's Q is loaded as soon as this one's is read
+        // how many keys this thread's rows see
+        int lim[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            lim[h] = row_h[h] < rows ? seen(w.req, (row0 + row_h[h]) / a.n_heads) : 0;
+        if (tid < rows) {
+            const int tok = (row0 + tid) / a.n_heads, head = row0 + tid - tok * a.n_heads;
+            sh.out[tid] = (w.req.q0 + tok) * a.ld_out_tok + head * a.ld_out_head;
+        }
+        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, z[2] = {0.0f, 0.0f};
+        if (vis > 0) {
             for (int t = 0; t < w.run; ++t, ++n) {
-                const int j0 = (w.off + t) * kTile;
+                const int j0 = (w.off + t) * kTile, c0 = j0 + 32 * half; // tile's, thread's first token
                 wait(&sh.s[n & 1], n >> 1);
                 fence_after();
-                float f[2] = {1.0f, 1.0f};
-                float x[32];
-                bool raise = false;
+                float x[16];
                 if (active) {
-                    ld16x64(x, tm_s + lanes + uint32_t(n & 1) * kTile);
+                    ld16x32(x, tm_s + lanes + uint32_t((n & 1) * kTile + 32 * half));
                     wait_ld();
                 }
                 fence_before();
                 bar_arrive(&sh.s_free[n & 1]);
+                if (ahead && t == w.run - 1)
+                    load_q<NR>(a, nx, sm + lay.q, warp, lane);
+                // Weights against the reference as it stands; whether any row has
+                // passed it is asked afterwards, so that no exponential waits
+                // for a maximum.
+                uint32_t p[2][4];
+                float sum[2] = {0.0f, 0.0f};
+                auto weigh = [&](int h) {
+                    const float ref = m[h] == -CUDART_INF_F ? 0.0f : m[h];
+                    float e[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        e[i] = ex2(fmaf(x[4 * (i >> 1) + 2 * h + (i & 1)], sl, -ref));
+                    sum[h] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        p[h][j] = pack_bf16(e[2 * j], e[2 * j + 1]);
+                };
+                auto store_p = [&] {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint8_t *to = sm + lay.p + row_h[h] * 128 + 4 * t4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint32_t *>(to + (((4 * half + j) ^ (row_h[h] & 7)) << 4)) = p[h][j];
+                    }
+                };
+                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+                bool raise = false;
                 if (active) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (j0 + kTile > lim[h]) {
+                        if (c0 + 32 > lim[h]) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (j0 + 8 * (i >> 1) + 2 * t4 + (i & 1) >= lim[h])
+                            for (int i = 0; i < 8; ++i)
+                                if (c0 + 8 * (i >> 1) + 2 * t4 + (i & 1) >= lim[h])
                                     x[4 * (i >> 1) + 2 * h + (i & 1)] = -CUDART_INF_F;
                         }
-                        float top[8];
+                        weigh(h);
+                        float top[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            top[i] = fmaxf(x[4 * i + 2 * h], x[4 * i + 2 * h + 1]);
-                        float mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
-                                         fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        mx *= sl;
-                        if (m[h] == -CUDART_INF_F) {
-                            m[h] = mx; // nothing summed yet
-                        } else if (mx > m[h] + kRaise) {
-                            f[h] = ex2(m[h] - mx);
-                            m[h] = mx;
-                            z[h] *= f[h];
-                            raise = true;
-                        }
-                        const float ref = m[h] == -CUDART_INF_F ? 0.0f : m[h];
-                        float sum[4] = {};
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float &e = x[4 * (i >> 1) + 2 * h + (i & 1)];
-                            e = ex2(fmaf(e, sl, -ref));
-                            sum[i & 3] += e;
-                        }
-                        z[h] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        for (int j = 0; j < 4; ++j)
+                            top[j] = fmaxf(x[4 * j + 2 * h], x[4 * j + 2 * h + 1]);
+                        mx[h] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl;
+                        // -inf + 8 is -inf: the first key that is seen raises it
+                        raise = raise || mx[h] > m[h] + kRaise;
                     }
                 }
                 // the last tile's second product has read P and written O
                 if (t > 0)
                     wait(&sh.o, n - 1);
-                if (active) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int row = 16 * warp + g4 + 8 * h;
-                        uint8_t *p = sm + lay.p + row * 128 + 4 * t4;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint32_t *>(p + ((j ^ (row & 7)) << 4)) =
-                                pack_bf16(x[4 * j + 2 * h], x[4 * j + 2 * h + 1]);
-                        if (t4 == 0)
-                            sh.f[row] = f[h];
-                    }
-                }
+                if (active)
+                    store_p();
                 if (j0 + kTile > vis) {
                     // rows of the tile that nobody sees may hold anything: their weights are 0, 0 x NaN is not
                     const int dead = kTile - (vis - j0);
                     for (int i = tid; i < dead * 64; i += kSoftThreads) {
                         const int c = i / (dead * 8), rest = i - c * dead * 8;
-                        uint8_t *half = c < kFront ? sm + lay.front + (n % lay.fronts * kFront + c) * kChunk
-                                                   : sm + lay.back + (n % lay.backs * kBack + c - kFront) * kChunk;
-                        *reinterpret_cast<uint4 *>(half + (vis - j0) * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+                        uint8_t *to = c < kFront ? sm + lay.front + (n % lay.fronts * kFront + c) * kChunk
+                                                 : sm + lay.back + (n % lay.backs * kBack + c - kFront) * kChunk;
+                        *reinterpret_cast<uint4 *>(to + (vis - j0) * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 if (sync_any(1, kSoftThreads, raise)) {
-                    fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < NR / 4; ++c) { // 16 columns: rows 16 c % NR .. of block 16 c / NR
-                        float o[16];
-                        ld32x16(o, tmem + lanes + uint32_t(16 * c));
-                        wait_ld();
+                    // the rows' maxima over both halves, the new references, the weights again
+                    if (active) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] *= sh.f[(16 * c) % NR + i];
-                        st32x16(tmem + lanes + uint32_t(16 * c), o);
+                        for (int h = 0; h < 2; ++h) {
+                            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                            if (t4 == 0)
+                                sh.top[half][row_h[h]] = mx[h];
+                        }
                     }
-                    wait_st();
+                    sync_some(1, kSoftThreads);
+                    if (active) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float all = fmaxf(sh.top[0][row_h[h]], sh.top[1][row_h[h]]);
+                            float f = 1.0f;
+                            if (all > m[h] + kRaise) {
+                                f = ex2(m[h] - all); // 0 from -inf: nothing is summed yet
+                                m[h] = all;
+                                z[h] *= f;
+                                weigh(h);
+                            }
+                            if (t4 == 0 && half == 0)
+                                sh.f[row_h[h]] = f;
+                        }
+                        store_p();
+                    }
+                    sync_some(1, kSoftThreads);
+                    if (t > 0) {
+                        fence_after();
+#pragma unroll 1
+                        for (int c = half; c < NR / 4; c += 2) { // 16 columns: rows 16 c % NR .. of block 16 c / NR
+                            float o[16];
+                            ld32x16(o, tmem + lanes + uint32_t(16 * c));
+                            wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] *= sh.f[(16 * c) % NR + i];
+                            st32x16(tmem + lanes + uint32_t(16 * c), o);
+                        }
+                        wait_st();
+                    }
                 }
+                z[0] += sum[0];
+                z[1] += sum[1];
                 fence_before();
                 fence_async_shared();
                 bar_arrive(&sh.p);
             }
-            wait(&sh.o, n - 1);
-            fence_after();
+            if (ahead) {
+                copy16_wait();
+                fence_async_shared();
+                bar_arrive(&sh.q);
+                loaded = true;
+            }
         }
         // ---- the run's result: the output, or a part of it
         const bool whole = w.off == 0 && w.run == w.tiles;
@@ -564,16 +616,22 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
         for (int h = 0; h < 2; ++h) {
             z[h] += __shfl_xor_sync(0xffffffffu, z[h], 1);
             z[h] += __shfl_xor_sync(0xffffffffu, z[h], 2);
-            const int row = 16 * warp + g4 + 8 * h;
-            if (active && t4 == 0) {
-                const bool some = z[h] > 0.0f || z[h] != z[h];
-                sh.inv[row] = some ? 1.0f / z[h] : 0.0f;
+            if (active && t4 == 0 && half == 1)
+                sh.top[1][row_h[h]] = z[h];
+        }
+        sync_some(1, kSoftThreads);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = row_h[h];
+            if (active && t4 == 0 && half == 0) {
+                const float zz = z[h] + sh.top[1][row];
+                const bool some = zz > 0.0f || zz != zz;
+                sh.f[row] = some ? 1.0f / zz : 0.0f;
                 if (row < rows) {
                     if (!whole)
-                        parts.mz[slot * kMaxRows + row] = make_float2(m[h], z[h]);
+                        parts.mz[slot * kMaxRows + row] = make_float2(m[h], zz);
                     else if (a.lse)
-                        a.lse[int64_t(w.req.q0) * a.n_heads + row0 + row] =
-                            some ? (m[h] + log2f(z[h])) * kLn2 : -CUDART_INF_F;
+                        a.lse[int64_t(w.req.q0) * a.n_heads + row0 + row] = some ? (m[h] + log2f(zz)) * kLn2 : -CUDART_INF_F;
                 }
             }
         }
@@ -588,41 +646,49 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
             b.first_slot = 2 * b.first + 1;
             parts.at[blockIdx.x] = b;
         }
+        if (vis > 0)
+            wait(&sh.o, n - 1);
+        fence_after();
         sync_some(1, kSoftThreads);
+        // warp halves take alternate runs of 16 rows, two runs' loads at a time
+        constexpr int kRuns = NR / 8; // of a warp
 #pragma unroll 1
-        for (int c = 0; c < NR / 4; ++c) {
-            const int n0 = (16 * c) % NR, d0 = 128 * (16 * c / NR) + 32 * warp;
-            if (n0 >= rows)
-                continue;
-            float o[16];
-            if (vis > 0) {
-                ld32x16(o, tmem + lanes + uint32_t(16 * c));
-                wait_ld();
-            } else {
+        for (int c0 = 0; c0 < kRuns; c0 += 2) {
+            float o[2][16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[i] = 0.0f;
-            }
-            if (whole) {
-                // lane pairs trade halves, so that each stores two columns of one row
+            for (int k = 0; k < 2; ++k)
+                if (vis > 0)
+                    ld32x16(o[k], tmem + lanes + uint32_t(16 * (2 * (c0 + k) + half)));
+            wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float e = o[i] * sh.inv[n0 + i], d = o[i + 1] * sh.inv[n0 + i + 1];
-                    const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? e : d, 1);
-                    const int row = n0 + i + (lane & 1);
-                    if (row < rows)
-                        *reinterpret_cast<uint32_t *>(a.out + sh.out[row] + d0 + (lane & ~1)) =
-                            lane & 1 ? pack_bf16(got, d) : pack_bf16(e, got);
+            for (int k = 0; k < 2; ++k) {
+                const int c = 2 * (c0 + k) + half, n0 = (16 * c) % NR, d0 = 128 * (16 * c / NR) + 32 * quarter;
+                if (n0 >= rows)
+                    continue;
+                if (whole) {
+                    // lane pairs trade halves, so that each stores two columns of one row
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float e = vis > 0 ? o[k][i] * sh.f[n0 + i] : 0.0f, d = vis > 0 ? o[k][i + 1] * sh.f[n0 + i + 1] : 0.0f;
+                        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? e : d, 1);
+                        const int row = n0 + i + (lane & 1);
+                        if (row < rows)
+                            *reinterpret_cast<uint32_t *>(a.out + sh.out[row] + d0 + (lane & ~1)) =
+                                lane & 1 ? pack_bf16(got, d) : pack_bf16(e, got);
+                    }
+                } else {
+                    float *to = parts.o + (size_t(slot) * kMaxRows + n0) * W8_LATENT_DIM + d0 + lane;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (n0 + i < rows)
+                            to[i * W8_LATENT_DIM] = o[k][i];
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (n0 + i < rows)
-                        parts.o[(size_t(slot) * kMaxRows + n0 + i) * W8_LATENT_DIM + d0 + lane] = o[i];
             }
         }
         fence_before(); // the loads of O, before the next run's products
         sync_some(1, kSoftThreads); // the rows' places and 1 / z are read
+        w = nx;
+        have = more;
     }
     return ok;
 }
@@ -668,14 +734,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         for (int r = r0; r < r1; ++r) {
             const Request q = r == r0 ? held : request_of(a, r);
             const int n = groups_of(q, a.n_heads, nr);
-            for (int g = 0; g < n; ++g)
-                sum += group_tiles(q, a.n_heads, nr, g);
+            if (q.q == 1) // all groups see the same
+                sum += int64_t(n) * max((q.len + kTile - 1) / kTile, 1);
+            else
+                for (int g = 0; g < n; ++g)
+                    sum += group_tiles(q, a.n_heads, nr, g);
         }
         return sum;
     };
     int rows = 0;
     for (int r = r0; r < r1; ++r)
-        rows = max(rows, min((r == r0 ? held : request_of(a, r)).q * a.n_heads, kMaxRows));
+        rows = max(rows, min((r == r0 ? held : request_of(a, r)).q * a.n_heads, kMaxRows + 1));
     // fewer rows a group: when no group would be filled, or when twice as many
     // groups still leave no SM two tiles (a count past 2^16 is many)
     rows = __reduce_max_sync(0xffffffffu, rows);
@@ -693,7 +762,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         all64 += sh.few[0][i];
         all32 += sh.few[1][i];
     }
-    const int grid = int(gridDim.x);
+    const int grid = int(gridDim.x), rows_max = rows;
     const int nr = rows > 32 && all64 * 2 > grid ? 64 : rows > 16 && all32 * 2 > grid ? 32 : 16;
     const int64_t mine = tiles_of(nr);
     int64_t inc = mine;
@@ -741,7 +810,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const int role = __shfl_sync(0xffffffffu, warp, 0);
     auto roles = [&](auto rows) {
         constexpr int NR = decltype(rows)::value;
-        return role == kCopyWarp    ? copy_role<NR>(a, map, w, sm, sh)
+        return role == kCopyWarp    ? copy_role<NR>(a, map, w, sm, sh, rows_max <= NR)
                : role == kScoreWarp ? score_role<NR>(a, w, sm, sh, tm_s)
                : role == kOutWarp   ? out_role<NR>(a, w, sm, sh, tmem)
                                     : softmax_role<NR>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid);
