@@ -1,85 +1,506 @@
 // w8_latent_expanded.cu -- latent attention, expanded form, over the keys and
 // values of a prompt (w8_latent_attn_expanded).
 //
-// The plainest form: a warp a (query token, head), one key after another, the
-// running maximum and sum of the softmax beside the output in registers.
+// With s = scale log2 e and a running reference m_i of query i,
+//   x_ij = q_i . k_j,  p_ij = 2^(s x_ij - m_i),  z_i = sum_j p_ij,
+//   out_i = sum_j p_ij v_j / z_i,  lse_i = (m_i + log2 z_i) ln 2.
+// A CTA takes 128 queries of one head and walks over the keys they see, 128 at
+// a time.  Both products run on tcgen05 with fp32 accumulators in tensor
+// memory:
+//   S [128 x 128] = Q K^T  (16 or 12 steps of 64 cycles)
+//   O [128 x d_v] += P V   (8 steps of 128 or 64 cycles), P as bf16 in tensor
+//     memory, in the columns of the S that it was made from.
+// S has two buffers, so that the scores of the next tile are made while the
+// weights of this one are.  With d_v = 256 the 512 columns are full: O 256,
+// S 2 x 128.
+//
+// Ten warps: 0-7 softmax (two threads a row, 64 keys each), 8 copies, 9
+// tensor-core issue.  Keys and values come by tensor-map copies into a ring of
+// equal slots, in the order in which the steps use them: K of tile 0, then K
+// of tile i + 1 and V of tile i in turn.  A K slot holds 128 keys x 64 or 128
+// columns, K-major; a V slot 64 keys x d_v columns, MN-major.  The parts of a
+// head's key (its own columns, the rope columns all heads share) meet only in
+// shared memory.
+//
+// The reference moves only when a row's maximum passes it by 2^8: the weights
+// are made against the reference as it stands, and a pair of warps redoes them
+// (and rescales its rows of O) when one of its rows has passed it.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
 
 #include "w8_device.cuh"
 #include "w8_serve_internal.h"
+#include "w8_tcgen.cuh"
 
 namespace w8 {
 
+__device__ int g_expanded_status;
+
 namespace {
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
+using namespace tcg;
+
+constexpr int kRows = 128, kKeys = 128;       // queries of a CTA, keys of a tile
+constexpr int kSoftWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kExpThreads = 320;
+constexpr int kSmem = 227 * 1024 - 2048;
+constexpr int kTmemCols = 512;
+constexpr float kRaise = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int DN, int DV>
-__global__ void __launch_bounds__(256) expanded_kernel(const w8_latent_expanded a)
+struct Shape {
+    static constexpr int kCols = DN + W8_LATENT_ROPE;      // of a query and a key
+    static constexpr int kChunks = kCols / 64;
+    static constexpr int kSlot = DV / 64 * 64 * 128;       // bytes
+    static constexpr int kKChunks = kSlot / (kKeys * 128); // 64-column chunks of a K slot
+    static constexpr int kKSlots = kChunks / kKChunks, kVSlots = kKeys / 64; // of a tile
+    static constexpr int kQ = kChunks * kRows * 128;
+    static constexpr int kSlots = (kSmem - 1024 - kQ) / kSlot;
+    static constexpr int kS = DV; // S's first column; O starts at 0
+    static_assert(kKSlots * kKChunks == kChunks && kS + 2 * kKeys <= kTmemCols && kSlots >= 4, "plan");
+};
+constexpr int kMaxSlots = 12;
+
+struct Shared {
+    uint64_t full[kMaxSlots], free_[kMaxSlots];
+    uint64_t q, s[2], p[2], o, end;
+    int count[kExpThreads / 32];
+    int found[6];
+    uint32_t tmem;
+    float top[2][kRows], z[kRows];
+};
+static_assert(sizeof(Shared) <= 2048, "shared memory");
+
+struct Maps {
+    CUtensorMap q_nope, q_rope, k_nope, k_rope, v;
+};
+
+// What a CTA works on.
+struct Item {
+    int q0, rows;   // first query token, queries (of the CTA)
+    int k0, nk;     // first key, keys of the request
+    int see0;       // keys that the first query sees, uncut; one more for each later one (causal)
+    int tiles;      // key tiles; 0: nothing is seen
+};
+
+__device__ __forceinline__ bool elect_one()
 {
-    constexpr int NQ = (DN + 64) / 32, NV = DV / 32;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= int64_t(a.n_q) * a.n_heads)
-        return;
-    const int t = int(row / a.n_heads), h = int(row - int64_t(t) * a.n_heads);
-    int r = 0;
-    while (r < a.n_req && a.cu_q[r + 1] <= t)
-        ++r;
-    if (r == a.n_req || a.cu_q[r] > t)
-        return;
-    const int q0 = max(a.cu_q[r], 0), q1 = min(a.cu_q[r + 1], a.n_q);
-    const int k0 = min(max(a.cu_k[r], 0), a.n_k), k1 = min(max(a.cu_k[r + 1], k0), a.n_k);
-    const int last = a.causal ? (k1 - k0) - (q1 - q0) + (t - q0) : k1 - k0 - 1;
-    float q[NQ], acc[NV] = {};
-    for (int i = 0; i < NQ; ++i)
-        q[i] = i < DN / 32 ? bf(a.q_nope[t * a.ld_qnope_tok + h * a.ld_qnope_head + i * 32 + lane])
-                           : bf(a.q_rope[t * a.ld_qrope_tok + h * a.ld_qrope_head + (i - DN / 32) * 32 + lane]);
-    float m = -CUDART_INF_F, z = 0.0f;
-    for (int j = k0; j <= k0 + last && j < k1; ++j) {
-        float x = 0.0f;
-        for (int i = 0; i < NQ; ++i) {
-            const float k = i < DN / 32 ? bf(a.k_nope[j * a.ld_knope_tok + h * a.ld_knope_head + i * 32 + lane])
-                                        : bf(a.k_rope[j * a.ld_krope_tok + (i - DN / 32) * 32 + lane]);
-            x = fmaf(q[i], k, x);
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+template <int DN, int DV>
+__global__ void __launch_bounds__(kExpThreads, 1)
+    expanded_kernel(const __grid_constant__ w8_latent_expanded a, const __grid_constant__ Maps maps, int tiles_max)
+{
+    using S = Shape<DN, DV>;
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    __shared__ __align__(16) Shared sh;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    uint8_t *const sm = s_dyn + ((1024u - (smem_addr(s_dyn) & 1023u)) & 1023u);
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            bar_init(&sh.full[i], 1);
+            bar_init(&sh.free_[i], 1);
         }
-        for (int d = 16; d > 0; d >>= 1)
-            x += __shfl_xor_sync(0xffffffffu, x, d);
-        x *= a.scale;
-        const float m1 = fmaxf(m, x), ref = m1 == -CUDART_INF_F ? 0.0f : m1; // NaN scores stay NaN
-        const float f = expf(m - ref), p = expf(x - ref);
-        m = m1;
-        z = z * f + p;
-        for (int i = 0; i < NV; ++i)
-            acc[i] = fmaf(p, bf(a.v[j * a.ld_v_tok + h * a.ld_v_head + i * 32 + lane]), acc[i] * f);
+        bar_init(&sh.q, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.s[i], 1);
+            bar_init(&sh.p[i], 32 * kSoftWarps);
+        }
+        bar_init(&sh.o, 1);
+        bar_init(&sh.end, 1);
+        bar_init_fence();
+        sh.found[0] = -1;
     }
-    for (int i = 0; i < NV; ++i) {
-        const float o = z > 0.0f || z != z ? acc[i] / z : 0.0f;
-        uint32_t u;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(0.0f), "f"(o));
-        a.out[t * a.ld_out_tok + h * a.ld_out_head + i * 32 + lane] = uint16_t(u);
+    if (warp == 0)
+        tmem_alloc(&sh.tmem, kTmemCols);
+    pdl_wait();
+
+    // ---- the item: query tile `want` of all requests' tiles, last ones first ----
+    const int head = int(blockIdx.x) / tiles_max;
+    const int want = tiles_max - 1 - (int(blockIdx.x) - head * tiles_max);
+    {
+        const int per = (a.n_req + kExpThreads - 1) / kExpThreads;
+        const int r0 = min(tid * per, a.n_req), r1 = min(r0 + per, a.n_req);
+        auto queries = [&](int r, int &q0) {
+            q0 = min(max(__ldg(a.cu_q + r), 0), a.n_q);
+            return min(max(__ldg(a.cu_q + r + 1), q0), a.n_q) - q0;
+        };
+        int mine = 0, q0;
+        for (int r = r0; r < r1; ++r)
+            mine += (queries(r, q0) + kRows - 1) / kRows;
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            inc += lane >= d ? o : 0;
+        }
+        if (lane == 31)
+            sh.count[warp] = inc;
+        __syncthreads();
+        int at = inc - mine;
+        for (int i = 0; i < warp; ++i)
+            at += sh.count[i];
+        for (int r = r0; r < r1; ++r) {
+            const int nq = queries(r, q0), n = (nq + kRows - 1) / kRows;
+            if (at <= want && want < at + n) {
+                const int k0 = min(max(__ldg(a.cu_k + r), 0), a.n_k);
+                const int nk = min(max(__ldg(a.cu_k + r + 1), k0), a.n_k) - k0;
+                const int i0 = (want - at) * kRows;
+                sh.found[0] = q0 + i0;
+                sh.found[1] = min(kRows, nq - i0);
+                sh.found[2] = k0;
+                sh.found[3] = nk;
+                sh.found[4] = a.causal ? nk - nq + i0 + 1 : nk;
+            }
+            at += n;
+        }
     }
-    if (a.lse && lane == 0)
-        a.lse[row] = (m == -CUDART_INF_F ? 0.0f : m) + logf(z);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sh.tmem, tm_s = tmem + S::kS;
+    Item it;
+    it.q0 = sh.found[0];
+    it.rows = sh.found[1];
+    it.k0 = sh.found[2];
+    it.nk = sh.found[3];
+    it.see0 = sh.found[4];
+    // keys that row i sees
+    auto sees = [&](int i) { return min(max(it.see0 + (a.causal ? i : 0), 0), it.nk); };
+    it.tiles = it.q0 < 0 ? 0 : (sees(it.rows - 1) + kKeys - 1) / kKeys;
+
+    bool ok = true;
+    if (it.q0 < 0) {
+        // fewer tiles than the grid allows for
+    } else if (warp == kCopyWarp) {
+        if (it.tiles > 0 && elect_one()) {
+            const uint32_t ring = smem_addr(sm + S::kQ), q = smem_addr(sm);
+            bar_expect(&sh.q, S::kQ);
+#pragma unroll
+            for (int c = 0; c < S::kChunks; ++c)
+                copy_box(q + c * kRows * 128, c < DN / 64 ? &maps.q_nope : &maps.q_rope, c < DN / 64 ? 64 * c : 0, head, it.q0,
+                         &sh.q, policy_normal());
+            int k = 0, used = 0;
+            uint32_t parity = 0;
+            auto slot = [&]() { // the next slot, its old content read
+                if (used >= S::kSlots)
+                    ok = ok && bar_wait(&sh.free_[k], parity ^ 1);
+                ++used;
+                return ok;
+            };
+            auto step = [&] {
+                if (++k == S::kSlots) {
+                    k = 0;
+                    parity ^= 1;
+                }
+            };
+            for (int i = 0; i <= it.tiles && ok; ++i) {
+                if (i < it.tiles) {
+#pragma unroll
+                    for (int g = 0; g < S::kKSlots; ++g) {
+                        if (!slot())
+                            break;
+                        bar_expect(&sh.full[k], S::kSlot);
+#pragma unroll
+                        for (int c = 0; c < S::kKChunks; ++c) {
+                            const int chunk = g * S::kKChunks + c;
+                            const uint32_t dst = ring + uint32_t(k * S::kSlot + c * kKeys * 128);
+                            if (chunk < DN / 64)
+                                copy_box(dst, &maps.k_nope, 64 * chunk, head, it.k0 + i * kKeys, &sh.full[k], policy_normal());
+                            else
+                                copy_box(dst, &maps.k_rope, 0, it.k0 + i * kKeys, &sh.full[k]);
+                        }
+                        step();
+                    }
+                }
+                if (i > 0) {
+#pragma unroll
+                    for (int g = 0; g < S::kVSlots; ++g) {
+                        if (!slot())
+                            break;
+                        bar_expect(&sh.full[k], S::kSlot);
+#pragma unroll
+                        for (int c = 0; c < DV / 64; ++c)
+                            copy_box(ring + uint32_t(k * S::kSlot + c * 64 * 128), &maps.v, 64 * c, head,
+                                     it.k0 + (i - 1) * kKeys + 64 * g, &sh.full[k], policy_normal());
+                        step();
+                    }
+                }
+            }
+            // the copies still in flight (there are any only after a wait elsewhere gave up)
+            if (!ok) {
+                bar_wait(&sh.q, 0);
+                --used; // the slot that was not to be had
+                for (int i = max(0, used - S::kSlots); i < used; ++i)
+                    bar_wait(&sh.full[i % S::kSlots], uint32_t((i / S::kSlots) & 1));
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (it.tiles > 0) {
+            constexpr uint32_t id_s = inst_desc(kRows, kKeys, false, false), id_o = inst_desc(kRows, DV, false, true);
+            const uint64_t dq = desc128_k(smem_addr(sm), 1024), dk = desc128_k(smem_addr(sm + S::kQ), 1024),
+                           dv = desc128(smem_addr(sm + S::kQ), 64 * 128, 1024);
+            const bool one = elect_one();
+            int k = 0;
+            uint32_t parity = 0;
+            auto wait = [&](uint64_t *bar, uint32_t ph) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, ph & 1)); };
+            auto step = [&] {
+                if (++k == S::kSlots) {
+                    k = 0;
+                    parity ^= 1;
+                }
+            };
+            wait(&sh.q, 0);
+            for (int i = 0; i <= it.tiles && ok; ++i) {
+                if (i < it.tiles) {
+                    // the second product of tile i - 2 has read its weights, in the same columns
+                    if (i >= 2)
+                        wait(&sh.o, uint32_t(i - 2));
+                    const uint32_t d = tm_s + uint32_t(i & 1) * kKeys;
+#pragma unroll
+                    for (int g = 0; g < S::kKSlots; ++g) {
+                        wait(&sh.full[k], parity);
+                        fence_after();
+                        const uint64_t b = dk + uint64_t((k * S::kSlot) >> 4);
+                        if (one && ok) {
+#pragma unroll
+                            for (int c = 0; c < 4 * S::kKChunks; ++c)
+                                mma_ss(d, dq + uint64_t((g * S::kKChunks * kRows * 128 + (c / 4) * kRows * 128 + (c % 4) * 32) >> 4),
+                                       b + uint64_t(((c / 4) * kKeys * 128 + (c % 4) * 32) >> 4), id_s, uint32_t(g | c));
+                            commit(&sh.free_[k]);
+                        }
+                        __syncwarp();
+                        step();
+                    }
+                    if (one)
+                        commit(&sh.s[i & 1]);
+                    __syncwarp();
+                }
+                if (i > 0) {
+                    const int t = i - 1;
+                    wait(&sh.p[t & 1], uint32_t(t >> 1));
+                    const uint32_t p = tm_s + uint32_t(t & 1) * kKeys;
+#pragma unroll
+                    for (int g = 0; g < S::kVSlots; ++g) {
+                        wait(&sh.full[k], parity);
+                        fence_after();
+                        const uint64_t b = dv + uint64_t((k * S::kSlot) >> 4);
+                        if (one && ok) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                mma_ts(tmem, p + uint32_t(64 * g + 8 * c), b + uint64_t((c * 2048) >> 4), id_o, uint32_t(t | g | c));
+                            commit(&sh.free_[k]);
+                        }
+                        __syncwarp();
+                        step();
+                    }
+                    if (one)
+                        commit(&sh.o);
+                    __syncwarp();
+                }
+            }
+            // nothing is in the tensor cores when the CTA frees its memory
+            if (one)
+                commit(&sh.end);
+            __syncwarp();
+            ok = bar_wait(&sh.end, 0) && ok;
+        }
+    } else {
+        // ---- softmax, output: thread (row, half) ------------------------------------
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const float sl = a.scale * kLog2e;
+        const uint32_t lanes = uint32_t(32 * quarter) << 16;
+        const int lim = row < it.rows ? sees(row) : 0;
+        auto wait = [&](uint64_t *bar, int ph) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, uint32_t(ph & 1))); };
+        float m = -CUDART_INF_F, z = 0.0f;
+        for (int t = 0; t < it.tiles; ++t) {
+            const int j0 = t * kKeys + 64 * half;
+            const uint32_t col = tm_s + lanes + uint32_t((t & 1) * kKeys + 64 * half);
+            wait(&sh.s[t & 1], t >> 1);
+            fence_after();
+            float x[64];
+            ld32x32(&x[0], col);
+            ld32x32(&x[32], col + 32);
+            wait_ld();
+            if (j0 + 64 > lim) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (j0 + i >= lim)
+                        x[i] = -CUDART_INF_F;
+            }
+            float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int i = 4; i < 64; ++i)
+                top[i & 3] = fmaxf(top[i & 3], x[i]);
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl;
+            // -inf + 8 is -inf: the first key that is seen raises it
+            if (sync_any(1 + quarter, 64, t == 0 || mx > m + kRaise)) {
+                sh.top[half][row] = mx;
+                sync_some(1 + quarter, 64);
+                const float all = fmaxf(mx, sh.top[half ^ 1][row]);
+                float f = 1.0f;
+                if (t == 0) {
+                    m = all;
+                } else if (all > m + kRaise) {
+                    f = ex2(m - all); // 0 from -inf: nothing is summed yet
+                    m = all;
+                    z *= f;
+                }
+                if (t > 0) {
+                    wait(&sh.o, t - 1);
+                    fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < DV / 2; c += 32) {
+                        float o[32];
+                        ld32x32(o, tmem + lanes + uint32_t(DV / 2 * half + c));
+                        wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= f;
+                        st32x32(tmem + lanes + uint32_t(DV / 2 * half + c), o);
+                    }
+                    wait_st();
+                }
+                sync_some(1 + quarter, 64); // sh.top is read
+            }
+            const float ref = m == -CUDART_INF_F ? 0.0f : m;
+            float sum[4] = {};
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float e0 = ex2(fmaf(x[2 * i], sl, -ref)), e1 = ex2(fmaf(x[2 * i + 1], sl, -ref));
+                sum[i & 3] += e0 + e1;
+                p[i] = pack_bf16(e0, e1);
+            }
+            z += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            st32x32u(col, p); // over this thread's own scores
+            wait_st();
+            if (t == it.tiles - 1 && it.nk < it.tiles * kKeys) {
+                // values past the request's keys may be anything: their weights are 0, 0 x NaN is not
+                const int first = it.nk - t * kKeys, slot0 = it.tiles * S::kKSlots + t * S::kVSlots;
+                for (int g = first / 64; g < S::kVSlots; ++g) {
+                    const int k = (slot0 + g) % S::kSlots;
+                    wait(&sh.full[k], (slot0 + g) / S::kSlots);
+                    const int from = max(first - 64 * g, 0), n = (64 - from) * 8; // 16-byte vectors of a run
+                    for (int i = tid; i < n * (DV / 64); i += 32 * kSoftWarps)
+                        *reinterpret_cast<uint4 *>(sm + S::kQ + k * S::kSlot + i / n * 64 * 128 + from * 128 + i % n * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();
+            }
+            fence_before();
+            bar_arrive(&sh.p[t & 1]);
+        }
+        // one use after the other: of the last two, either may be open still
+        if (it.tiles > 1)
+            wait(&sh.o, it.tiles - 2);
+        if (it.tiles > 0)
+            wait(&sh.o, it.tiles - 1);
+        fence_after();
+        if (half == 1)
+            sh.z[row] = z;
+        else
+            sh.top[0][row] = z;
+        sync_some(1 + quarter, 64);
+        z = sh.top[0][row] + sh.z[row];
+        const bool some = z > 0.0f || z != z;
+        const float inv = some ? 1.0f / z : 0.0f;
+        const int64_t tok = it.q0 + row;
+        if (row < it.rows && half == 0 && a.lse)
+            a.lse[tok * a.n_heads + head] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
+        uint16_t *out = a.out + tok * a.ld_out_tok + head * a.ld_out_head + DV / 2 * half;
+#pragma unroll 1
+        for (int c = 0; c < DV / 2; c += 32) {
+            float o[32];
+            if (it.tiles > 0) {
+                ld32x32(o, tmem + lanes + uint32_t(DV / 2 * half + c));
+                wait_ld();
+            }
+            if (row < it.rows) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (it.tiles > 0) {
+                        u.x = pack_bf16(o[8 * v] * inv, o[8 * v + 1] * inv);
+                        u.y = pack_bf16(o[8 * v + 2] * inv, o[8 * v + 3] * inv);
+                        u.z = pack_bf16(o[8 * v + 4] * inv, o[8 * v + 5] * inv);
+                        u.w = pack_bf16(o[8 * v + 6] * inv, o[8 * v + 7] * inv);
+                    }
+                    *reinterpret_cast<uint4 *>(out + c + 8 * v) = u;
+                }
+            }
+        }
+    }
+    if (!ok)
+        atomicOr(&g_expanded_status, 1);
+    pdl_launch_dependents();
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        tmem_free(tmem, kTmemCols);
+    }
+}
+
+// [toks][heads][cols] read in boxes of 64 columns x 1 head x `rows` tokens.
+bool map_heads(CUtensorMap *m, const uint16_t *p, int toks, int heads, int cols, int64_t ld_tok, int64_t ld_head, int rows)
+{
+    const uint64_t sizes[3] = {uint64_t(cols), uint64_t(heads), uint64_t(toks)};
+    const uint64_t strides[2] = {uint64_t(ld_head) * 2, uint64_t(ld_tok) * 2};
+    const uint32_t box[3] = {64, 1, uint32_t(rows)};
+    return encode_bf16_map(m, p, 3, sizes, strides, box);
+}
+
+template <int DN, int DV>
+cudaError_t launch(const w8_latent_expanded &a, cudaStream_t s)
+{
+    auto *fn = &expanded_kernel<DN, DV>;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
+    Maps maps;
+    bool ok = map_heads(&maps.q_nope, a.q_nope, a.n_q, a.n_heads, DN, a.ld_qnope_tok, a.ld_qnope_head, kRows) &&
+              map_heads(&maps.q_rope, a.q_rope, a.n_q, a.n_heads, W8_LATENT_ROPE, a.ld_qrope_tok, a.ld_qrope_head, kRows);
+    if (a.n_k > 0) { // without keys nothing is copied
+        const uint64_t sizes[2] = {W8_LATENT_ROPE, uint64_t(a.n_k)}, strides[1] = {uint64_t(a.ld_krope_tok) * 2};
+        const uint32_t box[2] = {64, kKeys};
+        ok = ok && map_heads(&maps.k_nope, a.k_nope, a.n_k, a.n_heads, DN, a.ld_knope_tok, a.ld_knope_head, kKeys) &&
+             map_heads(&maps.v, a.v, a.n_k, a.n_heads, DV, a.ld_v_tok, a.ld_v_head, 64) &&
+             encode_bf16_map(&maps.k_rope, a.k_rope, 2, sizes, strides, box);
+    } else {
+        maps.k_nope = maps.v = maps.k_rope = maps.q_rope;
+    }
+    if (!ok)
+        return cudaErrorInvalidValue;
+    // query tiles: every request may end in a part of one
+    const int64_t tiles = a.n_q / kRows + (a.n_req < a.n_q ? a.n_req : a.n_q);
+    if (tiles * a.n_heads > INT32_MAX)
+        return cudaErrorInvalidValue;
+    return launch_dependent(fn, dim3(unsigned(tiles * a.n_heads)), kExpThreads, kSmem, s, a, maps, int(tiles));
 }
 
 } // namespace
 
-cudaError_t expanded_status(int *out, bool)
-{
-    *out = 0;
-    return cudaSuccess;
-}
-
 cudaError_t launch_latent_expanded(const w8_latent_expanded &a, int, cudaStream_t s)
 {
-    const int64_t rows = int64_t(a.n_q) * a.n_heads;
-    auto *fn = a.d_nope == 192 ? &expanded_kernel<192, 256> : &expanded_kernel<128, 128>;
-    return launch_dependent(fn, dim3(unsigned((rows + 7) / 8)), 256, 0, s, a);
+    return a.d_nope == 192 ? launch<192, 256>(a, s) : launch<128, 128>(a, s);
+}
+
+cudaError_t expanded_status(int *out, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_expanded_status, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_expanded_status, &zero, sizeof(int));
+    }
+    return e;
 }
 
 } // namespace w8

@@ -181,7 +181,7 @@ struct Shared {
     uint64_t q, s[2], s_free[2], p, o, end[2];
     int64_t out[kMaxRows]; // a row's place in the output
     int64_t sum[kPagedThreads / 32];
-    int max[kPagedThreads / 32], few[2][kPagedThreads / 32];
+    int max[kPagedThreads / 32], few[kPagedThreads / 32];
     int start[3];
     uint32_t tmem;
     float f[kMaxRows], top[2][kMaxRows];
@@ -495,7 +495,7 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                 // passed it is asked afterwards, so that no exponential waits
                 // for a maximum.
                 uint32_t p[2][4];
-                float sum[2] = {0.0f, 0.0f};
+                float sum[2];
                 auto weigh = [&](int h) {
                     const float ref = m[h] == -CUDART_INF_F ? 0.0f : m[h];
                     float e[8];
@@ -527,7 +527,8 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                                 if (c0 + 8 * (i >> 1) + 2 * t4 + (i & 1) >= lim[h])
                                     x[4 * (i >> 1) + 2 * h + (i & 1)] = -CUDART_INF_F;
                         }
-                        weigh(h);
+                        if (t > 0) // the first tile's reference is not known yet
+                            weigh(h);
                         float top[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -538,10 +539,11 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                     }
                 }
                 // the last tile's second product has read P and written O
-                if (t > 0)
+                if (t > 0) {
                     wait(&sh.o, n - 1);
-                if (active)
-                    store_p();
+                    if (active)
+                        store_p();
+                }
                 if (j0 + kTile > vis) {
                     // rows of the tile that nobody sees may hold anything: their weights are 0, 0 x NaN is not
                     const int dead = kTile - (vis - j0);
@@ -552,7 +554,7 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                         *reinterpret_cast<uint4 *>(to + (vis - j0) * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
-                if (sync_any(1, kSoftThreads, raise)) {
+                if (sync_any(1, kSoftThreads, raise || t == 0)) {
                     // the rows' maxima over both halves, the new references, the weights again
                     if (active) {
 #pragma unroll
@@ -569,12 +571,14 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                         for (int h = 0; h < 2; ++h) {
                             const float all = fmaxf(sh.top[0][row_h[h]], sh.top[1][row_h[h]]);
                             float f = 1.0f;
-                            if (all > m[h] + kRaise) {
-                                f = ex2(m[h] - all); // 0 from -inf: nothing is summed yet
+                            if (t == 0) {
+                                m[h] = all;
+                            } else if (all > m[h] + kRaise) { // from -inf: nothing is summed yet, f is 0
+                                f = ex2(m[h] - all);
                                 m[h] = all;
                                 z[h] *= f;
-                                weigh(h);
                             }
+                            weigh(h);
                             if (t4 == 0 && half == 0)
                                 sh.f[row_h[h]] = f;
                         }
@@ -596,8 +600,10 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                         wait_st();
                     }
                 }
-                z[0] += sum[0];
-                z[1] += sum[1];
+                if (active) {
+                    z[0] += sum[0];
+                    z[1] += sum[1];
+                }
                 fence_before();
                 fence_async_shared();
                 bar_arrive(&sh.p);
@@ -746,25 +752,24 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     for (int r = r0; r < r1; ++r)
         rows = max(rows, min((r == r0 ? held : request_of(a, r)).q * a.n_heads, kMaxRows + 1));
     // fewer rows a group: when no group would be filled, or when twice as many
-    // groups still leave no SM two tiles (a count past 2^16 is many)
+    // groups still leave no SM two tiles (a thread's count past 2^16 is many)
     rows = __reduce_max_sync(0xffffffffu, rows);
-    const int n64 = __reduce_add_sync(0xffffffffu, int(min(tiles_of(64), int64_t(1 << 16))));
-    const int n32 = __reduce_add_sync(0xffffffffu, int(min(tiles_of(32), int64_t(1 << 16))));
+    int64_t mine = tiles_of(64);
+    const int few = __reduce_add_sync(0xffffffffu, int(min(mine, int64_t(1 << 16))));
     if (lane == 0) {
         sh.max[warp] = rows;
-        sh.few[0][warp] = n64;
-        sh.few[1][warp] = n32;
+        sh.few[warp] = few;
     }
     __syncthreads();
-    int all64 = 0, all32 = 0;
+    int all64 = 0;
     for (int i = 0; i < kPagedThreads / 32; ++i) {
         rows = max(rows, sh.max[i]);
-        all64 += sh.few[0][i];
-        all32 += sh.few[1][i];
+        all64 += sh.few[i];
     }
     const int grid = int(gridDim.x), rows_max = rows;
-    const int nr = rows > 32 && all64 * 2 > grid ? 64 : rows > 16 && all32 * 2 > grid ? 32 : 16;
-    const int64_t mine = tiles_of(nr);
+    const int nr = rows > 32 && all64 * 2 > grid ? 64 : rows > 16 && all64 * 4 > grid ? 32 : 16;
+    if (nr != 64)
+        mine = tiles_of(nr);
     int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -781,8 +786,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     }
     const int64_t ctas = min(total, int64_t(gridDim.x)); // those that have work
     Walk w{};
-    w.pos = ctas ? min(int64_t(blockIdx.x), ctas) * total / ctas : 0;
-    w.end = ctas ? min(int64_t(blockIdx.x) + 1, ctas) * total / ctas : 0;
+    if (total * ctas < int64_t(1) << 32) { // 64-bit division is a call of some hundred instructions
+        const uint32_t t = uint32_t(total), c = uint32_t(ctas);
+        w.pos = c ? min(blockIdx.x, c) * t / c : 0;
+        w.end = c ? min(blockIdx.x + 1, c) * t / c : 0;
+    } else {
+        w.pos = min(int64_t(blockIdx.x), ctas) * total / ctas;
+        w.end = min(int64_t(blockIdx.x) + 1, ctas) * total / ctas;
+    }
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
         int64_t at = before;
         for (int r = r0; r < r1; ++r) {

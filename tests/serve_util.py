@@ -9,7 +9,8 @@ its magnitude, X = max_j scale sum_d |q_d k_jd|, D columns, L keys:
   shifted argument of the exponential, so a weight by a factor 1 + e with
   e = 1.1 (g X + 4 u X) + 2^-21 (the exponential itself);
   the quotient of two such sums by at most 2 e and the sums' own 2 L u each;
-  a weight's rounding to bf16 adds 2^-9 of A, the output's 2^-9 of |O|.
+  a weight's rounding to bf16 (8 significant bits: half a unit is at most 2^-8
+  of the value) adds 2^-8 of A, the output's 2^-8 of |O|.
 """
 from __future__ import annotations
 
@@ -38,7 +39,7 @@ def attend64(q, k, v, scale, see):
 
 def out_bound(o, a, x, cols, keys):
     e = 1.1 * (2 * (cols + 2) * U * x + 4 * U * x) + 2.0 ** -21
-    return 2.0 ** -9 * o.abs() * (1 + 2.0 ** -7) + (2.0 ** -9 + 2 * e[..., None] + 4 * keys * U) * a * (1 + 2.0 ** -7) + 1e-30
+    return 2.0 ** -8 * o.abs() * (1 + 2.0 ** -7) + (2.0 ** -8 + 2 * e[..., None] + 4 * keys * U) * a * (1 + 2.0 ** -7) + 1e-30
 
 
 def lse_bound(lse, x, cols, keys):
