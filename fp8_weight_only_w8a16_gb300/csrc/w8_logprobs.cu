@@ -13,10 +13,12 @@
 //
 // The alternatives: a logit's 32-bit value in order, then the inverted token
 // number, make one 64-bit key, so all keys differ and equal logits rank by the
-// lowest token.  A warp holds its best 32 keys sorted, one a lane; a vector of
-// logits is looked at only when its maximum (needed for m anyway) passes the
-// warp's `top`-th key, which for unordered logits happens about
-// top ln(n / top) times over n logits.
+// lowest token.  A thread keeps the largest value of what it has read (the sums
+// need the vectors' maxima anyway).  From the threads' largest values comes a
+// bound that at least `top` logits reach; the few threads that reach it have
+// their vectors read once more, the keys that pass are gathered, and a key's
+// place is the number of larger keys gathered.  The loop over the logits knows
+// nothing of the selection.
 //
 // A row is cut into `splits` runs of whole 16-byte vectors, one a CTA; the
 // last CTA of a row to arrive joins the runs in order of their number.
@@ -33,14 +35,14 @@ namespace w8 {
 namespace {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpAhead = 4; // vectors a thread has in flight
+constexpr int kLpAhead = 4; // vectors a thread has in flight beside those it works on
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e38f;
 
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // The larger of the two; NaN if either is.
@@ -90,27 +92,40 @@ __device__ __forceinline__ uint64_t key_of(float x, int token)
 }
 __device__ __forceinline__ int token_of(uint64_t key) { return int(~uint32_t(key)); }
 
-// A warp's best keys, lane l the l-th; 0 where there is none yet.
-struct Best {
-    uint64_t key;  // this lane's
-    uint64_t last; // the `top`-th
-};
-// Offers one key a lane (0: none).
-__device__ __forceinline__ void best_offer(Best &b, uint64_t key, int top, int lane)
+// Two floats in one register pair.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
 {
-    uint32_t who;
-    while ((who = __ballot_sync(0xffffffffu, key > b.last)) != 0) {
-        const int src = __ffs(int(who)) - 1;
-        const uint64_t k = __shfl_sync(0xffffffffu, key, src);
-        const int at = __popc(__ballot_sync(0xffffffffu, b.key > k));
-        const uint64_t up = __shfl_up_sync(0xffffffffu, b.key, 1);
-        b.key = lane < at ? b.key : lane == at ? k : up;
-        b.last = __shfl_sync(0xffffffffu, b.key, top - 1);
-        if (lane == src)
-            key = 0;
-    }
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 pair_values(uint64_t p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
+// 16 bytes of logits: their number, values, largest and smallest (of those
+// that are not NaN).
 template <typename T>
 struct Vec;
 template <>
@@ -125,9 +140,39 @@ struct Vec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
         }
     }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void range(float &lo, float &hi, const uint4 &v, const float (&)[8])
+    {
+        const uint32_t a = max2(max2(v.x, v.y), max2(v.z, v.w)), b = min2(min2(v.x, v.y), min2(v.z, v.w));
+        hi = fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+        lo = fminf(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+    }
     static __device__ __forceinline__ float one(const void *p, int64_t i)
     {
         return __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p) + i)) << 16);
+    }
+    static __device__ __forceinline__ float held(const void *p, int i)
+    {
+        return __uint_as_float(uint32_t(static_cast<const uint16_t *>(p)[i]) << 16);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8])
+    {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = __float_as_uint(x[2 * i]) >> 16 | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
+        return make_uint4(u[0], u[1], u[2], u[3]);
     }
 };
 template <>
@@ -140,9 +185,19 @@ struct Vec<float> {
         x[2] = __uint_as_float(v.z);
         x[3] = __uint_as_float(v.w);
     }
+    static __device__ __forceinline__ void range(float &lo, float &hi, const uint4 &, const float (&x)[4])
+    {
+        hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+    }
     static __device__ __forceinline__ float one(const void *p, int64_t i)
     {
         return __ldg(static_cast<const float *>(p) + i);
+    }
+    static __device__ __forceinline__ float held(const void *p, int i) { return static_cast<const float *>(p)[i]; }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4])
+    {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
 };
 
@@ -155,44 +210,103 @@ __device__ __forceinline__ uint4 ld_once(const void *p)
     return v;
 }
 
-// n logits x[], tokens t0 .. (those with t0 + i outside [lo, hi) left out).
-template <bool kTop, int N>
-__device__ __forceinline__ void take(Stat &s, Best &b, const float (&x)[N], int t0, bool all, int lo, int hi,
-                                     int top, int lane, bool live)
+// A vector's share of the sums; `z` and `w` in pairs.
+template <typename T>
+__device__ __forceinline__ void take(Stat &s, uint64_t &z, uint64_t &w, const uint4 &raw, float &hi)
 {
-    float mx = x[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-        mx = fmaxf(mx, x[i]);
-    if (live) {
-        if (mx > s.m)
-            stat_raise(s, mx);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float d = max_nan((x[i] - s.m) * kLog2e, -1000.0f), e = ex2(d);
-            s.z += e;
-            s.w = fmaf(e, d, s.w);
-        }
+    constexpr int N = Vec<T>::n;
+    float x[N], lo;
+    Vec<T>::widen(x, raw);
+    Vec<T>::range(lo, hi, raw, x);
+    if (hi > s.m) { // a new reference
+        const float2 a = pair_values(z), b = pair_values(w);
+        s.z = a.x + a.y;
+        s.w = b.x + b.y;
+        stat_raise(s, hi);
+        z = pair_of(s.z, 0.0f);
+        w = pair_of(s.w, 0.0f);
     }
-    if constexpr (kTop) {
-        // no warp-mate's vector passes the `top`-th value: the usual case (a
-        // later token of the same value would rank behind; while the list is
-        // not full its last key is 0, whose value is NaN, so everything passes)
-        const bool pass = live && !(mx <= value_of(uint32_t(b.last >> 32)));
-        if (__any_sync(0xffffffffu, pass)) {
+    const uint64_t minus = pair_of(-s.m, -s.m), scale = pair_of(kLog2e, kLog2e);
+    if ((lo - s.m) * kLog2e >= -1000.0f) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                best_offer(b, pass && (all || (t0 + i >= lo && t0 + i < hi)) ? key_of(x[i], t0 + i) : 0, top, lane);
+        for (int i = 0; i < N; i += 2) {
+            const uint64_t d = pair_mul(pair_add(pair_of(x[i], x[i + 1]), minus), scale);
+            const float2 v = pair_values(d);
+            const uint64_t e = pair_of(ex2(v.x), ex2(v.y));
+            z = pair_add(z, e);
+            w = pair_fma(e, d, w);
+        }
+    } else { // banned tokens, or a masked value far below: 0 x infinity is kept out of w
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float d0 = max_nan((x[i] - s.m) * kLog2e, -1000.0f), d1 = max_nan((x[i + 1] - s.m) * kLog2e, -1000.0f);
+            const uint64_t e = pair_of(ex2(d0), ex2(d1));
+            z = pair_add(z, e);
+            w = pair_fma(e, pair_of(d0, d1), w);
         }
     }
 }
 
+// Gathered keys, and what the selection shares.
+constexpr int kGather = 256;
+struct Select {
+    uint64_t key[kGather];
+    uint64_t best[W8_MAX_TOP];
+    uint64_t bound;      // keys from here on are gathered
+    uint32_t nth[kLpWarps];
+    int count, passing;
+    uint8_t thread[kLpThreads]; // those whose largest value reaches the bound
+};
+
+// best[0 .. top - 1] = the largest of the keys that `scan` offers, in falling
+// order (0 where there are fewer), over all threads of the CTA.  scan(offer)
+// calls offer(key) for every key that may count, and offers the same keys
+// whenever it is called; at least `top` of them reach sel.bound, if there are
+// that many.  When more pass than there is room for, the `top`-th of those
+// gathered is the next bound: an eighth of them or less pass it.
+template <typename Scan>
+__device__ __forceinline__ void select_top(Select &sel, int top, int tid, const Scan &scan)
+{
+    for (;;) {
+        if (tid == 0)
+            sel.count = 0;
+        if (tid < top)
+            sel.best[tid] = 0;
+        __syncthreads();
+        const uint64_t bound = sel.bound;
+        scan([&](uint64_t key) {
+            if (key >= bound && key != 0) {
+                const int at = atomicAdd(&sel.count, 1);
+                if (at < kGather)
+                    sel.key[at] = key;
+            }
+        });
+        __syncthreads();
+        const int n = min(sel.count, kGather);
+        const bool more = sel.count > kGather;
+        if (tid < n) {
+            const uint64_t mine = sel.key[tid];
+            int rank = 0;
+            for (int i = 0; i < n; ++i)
+                rank += sel.key[i] > mine;
+            if (rank < top)
+                sel.best[rank] = mine;
+        }
+        __syncthreads();
+        if (!more)
+            return;
+        if (tid == 0)
+            sel.bound = sel.best[top - 1];
+        __syncthreads();
+    }
+}
+
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs a)
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobsArgs a)
 {
     constexpr int N = Vec<T>::n;
     __shared__ Stat s_stat[kLpWarps];
-    __shared__ uint64_t s_key[kLpWarps][32];
+    __shared__ Select sel;
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / a.splits;
@@ -206,32 +320,52 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     const int skew = int((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
     const int nvec = (a.vocab + skew + N - 1) / N;
     const int v0 = int(int64_t(split) * nvec / a.splits), v1 = int(int64_t(split + 1) * nvec / a.splits);
-    Stat s{kLowest, 0.0f, 0.0f};
-    Best b{0, 0};
-    for (int base = v0; base < v1; base += kLpThreads * kLpAhead) {
-        uint4 raw[kLpAhead];
-#pragma unroll
-        for (int k = 0; k < kLpAhead; ++k) {
-            const int v = base + k * kLpThreads + tid, t0 = v * N - skew;
-            raw[k] = make_uint4(0, 0, 0, 0);
-            if (v < v1 && t0 >= 0 && t0 + N <= a.vocab)
-                raw[k] = ld_once(x + t0);
-        }
-#pragma unroll
-        for (int k = 0; k < kLpAhead; ++k) {
-            const int v = base + k * kLpThreads + tid, t0 = v * N - skew;
-            if (base + k * kLpThreads + (tid & ~31) >= v1)
-                break; // nothing for the whole warp
-            const bool live = v < v1, all = t0 >= 0 && t0 + N <= a.vocab;
-            float f[N];
-            Vec<T>::widen(f, raw[k]);
-            if (live && !all) {
+    const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u; // -inf
+    // a vector, -inf where there is no token
+    auto load = [&](int v) {
+        const int t0 = v * N - skew;
+        uint4 raw = make_uint4(none, none, none, none);
+        if (v < v1) {
+            if (t0 >= 0 && t0 + N <= a.vocab) {
+                raw = ld_once(x + t0);
+            } else {
+                float f[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     f[i] = t0 + i >= 0 && t0 + i < a.vocab ? Vec<T>::one(x, t0 + i) : -CUDART_INF_F;
+                raw = Vec<T>::pack(f);
             }
-            take<kTop, N>(s, b, f, t0, all, 0, a.vocab, a.top, lane, live);
         }
+        return raw;
+    };
+    Stat s{kLowest, 0.0f, 0.0f};
+    uint64_t z = pair_of(0.0f, 0.0f), w = z;
+    float top_value = CUDART_NAN_F; // the largest read so far; passed by anything at first
+    uint4 raw[kLpAhead];
+#pragma unroll
+    for (int k = 0; k < kLpAhead; ++k)
+        raw[k] = load(v0 + k * kLpThreads + tid);
+    for (int base = v0; base < v1; base += kLpThreads * kLpAhead) {
+        uint4 now[kLpAhead];
+#pragma unroll
+        for (int k = 0; k < kLpAhead; ++k) {
+            now[k] = raw[k];
+            raw[k] = load(base + (kLpAhead + k) * kLpThreads + tid);
+        }
+        float hi[kLpAhead];
+#pragma unroll
+        for (int k = 0; k < kLpAhead; ++k)
+            take<T>(s, z, w, now[k], hi[k]);
+        if constexpr (kTop) {
+            const float most = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+            if (!(most <= top_value))
+                top_value = most;
+        }
+    }
+    {
+        const float2 zz = pair_values(z), ww = pair_values(w);
+        s.z = zz.x + zz.y;
+        s.w = ww.x + ww.y;
     }
 
     // the warp's, then the CTA's result
@@ -245,22 +379,69 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
             stat_join(st, o);
         }
     };
-    auto cta_join = [&]() {
+    auto cta_join = [&]() { // into warp 0
         warp_join(s);
         if (lane == 0)
             s_stat[warp] = s;
-        if constexpr (kTop)
-            s_key[warp][lane] = b.key;
         __syncthreads();
         if (warp == 0) {
             s = lane < kLpWarps ? s_stat[lane] : Stat{kLowest, 0.0f, 0.0f};
             warp_join(s);
-            if constexpr (kTop)
-                for (int w = 1; w < kLpWarps; ++w)
-                    best_offer(b, lane < a.top ? s_key[w][lane] : 0, a.top, lane);
         }
     };
     cta_join();
+    if constexpr (kTop) {
+        // The bound: of the warps' k-th largest values (k = top / warps, rounded
+        // up), the c-th largest, c k >= top.  Warps that are not full of vectors
+        // have no say; without a full one (under 32 vectors) everything passes.
+        const int nv = v1 - v0, full = min(nv / 32, kLpWarps);
+        const uint32_t mine = tid < nv ? order_of(top_value) : 0;
+        uint64_t bound = 0;
+        if (full > 0) {
+            const int k = (a.top + full - 1) / full, c = (a.top + k - 1) / k;
+            uint32_t left = mine, nth = 0;
+            for (int i = 0; i < k; ++i) {
+                nth = __reduce_max_sync(0xffffffffu, left);
+                const uint32_t who = __ballot_sync(0xffffffffu, left == nth);
+                if (lane == __ffs(int(who)) - 1)
+                    left = 0;
+            }
+            if (lane == 0)
+                sel.nth[warp] = nth;
+            __syncthreads();
+            uint32_t own = lane < full ? sel.nth[lane] : 0;
+            int rank = 0;
+            for (int i = 0; i < full; ++i) {
+                const uint32_t o = __shfl_sync(0xffffffffu, own, i);
+                rank += o > own || (o == own && i < lane);
+            }
+            const uint32_t at = __ballot_sync(0xffffffffu, lane < full && rank == c - 1);
+            bound = uint64_t(__shfl_sync(0xffffffffu, own, __ffs(int(at)) - 1)) << 32;
+        }
+        if (tid == 0) {
+            sel.bound = bound;
+            sel.passing = 0;
+        }
+        __syncthreads();
+        if (tid < nv && uint64_t(mine) << 32 >= bound)
+            sel.thread[atomicAdd(&sel.passing, 1)] = uint8_t(tid);
+        __syncthreads();
+        const int per = (nv + kLpThreads - 1) / kLpThreads, pairs = sel.passing * per;
+        select_top(sel, a.top, tid, [&](auto &&offer) {
+            for (int i = tid; i < pairs; i += kLpThreads) {
+                const int j = i / per, v = v0 + (i - j * per) * kLpThreads + sel.thread[j], t0 = v * N - skew;
+                if (v < v1) {
+                    const uint4 u = load(v);
+                    float f[N];
+                    Vec<T>::widen(f, u);
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (t0 + e >= 0 && t0 + e < a.vocab)
+                            offer(key_of(f[e], t0 + e));
+                }
+            }
+        });
+    }
     if (a.splits > 1) {
         LogprobsPart *parts = a.parts + row * a.splits;
         if (warp == 0) {
@@ -270,7 +451,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
                 parts[split].w = s.w;
             }
             if (kTop && lane < a.top)
-                parts[split].key[lane] = b.key;
+                parts[split].key[lane] = sel.best[lane];
             __threadfence();
         }
         __syncthreads();
@@ -281,12 +462,29 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
             return;
         __threadfence();
         s = Stat{kLowest, 0.0f, 0.0f};
-        b = Best{0, 0};
         for (int i = tid; i < a.splits; i += kLpThreads)
             stat_join(s, Stat{__ldcg(&parts[i].m), __ldcg(&parts[i].z), __ldcg(&parts[i].w)});
-        if constexpr (kTop)
-            for (int i = warp; i < a.splits; i += kLpWarps)
-                best_offer(b, lane < a.top ? __ldcg(&parts[i].key[lane]) : 0, a.top, lane);
+        if constexpr (kTop) {
+            // the bound: of the runs' d-th keys, d = top / runs rounded up, the c-th largest, c d >= top
+            const int d = (a.top + a.splits - 1) / a.splits, c = (a.top + d - 1) / d;
+            for (int i = tid; i < a.splits; i += kLpThreads)
+                sel.key[i] = __ldcg(&parts[i].key[d - 1]);
+            __syncthreads();
+            if (tid < a.splits) {
+                const uint64_t mine = sel.key[tid];
+                int rank = 0;
+                for (int i = 0; i < a.splits; ++i)
+                    rank += sel.key[i] > mine || (sel.key[i] == mine && i < tid); // equal ones are empty
+                if (rank == c - 1)
+                    sel.bound = mine;
+            }
+            __syncthreads();
+            select_top(sel, a.top, tid, [&](auto &&offer) {
+#pragma unroll 4
+                for (int i = tid; i < a.splits * a.top; i += kLpThreads)
+                    offer(__ldcg(&parts[i / a.top].key[i % a.top]));
+            });
+        }
         cta_join();
         if (tid == 0)
             a.counters[row] = 0;
@@ -300,8 +498,10 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
                 a.entropy[row] = logz - s.w * kLn2 / s.z;
         }
         if (kTop && lane < a.top) {
-            a.top_ids[row * a.top + lane] = token_of(b.key);
-            a.top_logprobs[row * a.top + lane] = value_of(uint32_t(b.key >> 32)) - s.m - logz;
+            // a place that is left (a row of NaN) gets a token all the same
+            const uint64_t key = sel.best[lane];
+            a.top_ids[row * a.top + lane] = key ? token_of(key) : lane;
+            a.top_logprobs[row * a.top + lane] = key ? value_of(uint32_t(key >> 32)) - s.m - logz : CUDART_NAN_F;
         }
     }
 }
@@ -316,7 +516,7 @@ int logprobs_splits(int rows, int vocab, int sms)
     const int64_t want = (int64_t(sms) * 8 + rows - 1) / rows;
     const int64_t most = (int64_t(vocab) + 1023) / 1024;
     const int64_t s = want < most ? want : most;
-    return int(s < 1 ? 1 : s > sms ? sms : s);
+    return int(s < 1 ? 1 : s > sms ? sms : s > kGather ? kGather : s);
 }
 
 cudaError_t launch_logprobs(const LogprobsArgs &a, bool bf16, cudaStream_t s)
