@@ -152,9 +152,15 @@ struct Vec<__nv_bfloat16> {
         asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
-    static __device__ __forceinline__ void range(float &lo, float &hi, const uint4 &v, const float (&)[8])
+    template <int K>
+    static __device__ __forceinline__ void range(float &lo, float &hi, const uint4 (&v)[K])
     {
-        const uint32_t a = max2(max2(v.x, v.y), max2(v.z, v.w)), b = min2(min2(v.x, v.y), min2(v.z, v.w));
+        uint32_t a = v[0].x, b = v[0].x;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            a = max2(a, max2(max2(v[k].x, v[k].y), max2(v[k].z, v[k].w)));
+            b = min2(b, min2(min2(v[k].x, v[k].y), min2(v[k].z, v[k].w)));
+        }
         hi = fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
         lo = fminf(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
     }
@@ -185,10 +191,17 @@ struct Vec<float> {
         x[2] = __uint_as_float(v.z);
         x[3] = __uint_as_float(v.w);
     }
-    static __device__ __forceinline__ void range(float &lo, float &hi, const uint4 &, const float (&x)[4])
+    template <int K>
+    static __device__ __forceinline__ void range(float &lo, float &hi, const uint4 (&v)[K])
     {
-        hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+        lo = hi = __uint_as_float(v[0].x);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float x[4];
+            widen(x, v[k]);
+            hi = fmaxf(hi, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+            lo = fminf(lo, fminf(fminf(x[0], x[1]), fminf(x[2], x[3])));
+        }
     }
     static __device__ __forceinline__ float one(const void *p, int64_t i)
     {
@@ -210,14 +223,13 @@ __device__ __forceinline__ uint4 ld_once(const void *p)
     return v;
 }
 
-// A vector's share of the sums; `z` and `w` in pairs.
-template <typename T>
-__device__ __forceinline__ void take(Stat &s, uint64_t &z, uint64_t &w, const uint4 &raw, float &hi)
+// The sums take in K vectors; `z` and `w` in pairs.  hi: their largest value.
+template <typename T, int K>
+__device__ __forceinline__ void take(Stat &s, uint64_t &z, uint64_t &w, const uint4 (&raw)[K], float &hi)
 {
     constexpr int N = Vec<T>::n;
-    float x[N], lo;
-    Vec<T>::widen(x, raw);
-    Vec<T>::range(lo, hi, raw, x);
+    float lo;
+    Vec<T>::range(lo, hi, raw);
     if (hi > s.m) { // a new reference
         const float2 a = pair_values(z), b = pair_values(w);
         s.z = a.x + a.y;
@@ -229,20 +241,30 @@ __device__ __forceinline__ void take(Stat &s, uint64_t &z, uint64_t &w, const ui
     const uint64_t minus = pair_of(-s.m, -s.m), scale = pair_of(kLog2e, kLog2e);
     if ((lo - s.m) * kLog2e >= -1000.0f) {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const uint64_t d = pair_mul(pair_add(pair_of(x[i], x[i + 1]), minus), scale);
-            const float2 v = pair_values(d);
-            const uint64_t e = pair_of(ex2(v.x), ex2(v.y));
-            z = pair_add(z, e);
-            w = pair_fma(e, d, w);
+        for (int k = 0; k < K; ++k) {
+            float x[N];
+            Vec<T>::widen(x, raw[k]);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const uint64_t d = pair_mul(pair_add(pair_of(x[i], x[i + 1]), minus), scale);
+                const float2 v = pair_values(d);
+                const uint64_t e = pair_of(ex2(v.x), ex2(v.y));
+                z = pair_add(z, e);
+                w = pair_fma(e, d, w);
+            }
         }
     } else { // banned tokens, or a masked value far below: 0 x infinity is kept out of w
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float d0 = max_nan((x[i] - s.m) * kLog2e, -1000.0f), d1 = max_nan((x[i + 1] - s.m) * kLog2e, -1000.0f);
-            const uint64_t e = pair_of(ex2(d0), ex2(d1));
-            z = pair_add(z, e);
-            w = pair_fma(e, pair_of(d0, d1), w);
+        for (int k = 0; k < K; ++k) {
+            float x[N];
+            Vec<T>::widen(x, raw[k]);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float d0 = max_nan((x[i] - s.m) * kLog2e, -1000.0f), d1 = max_nan((x[i + 1] - s.m) * kLog2e, -1000.0f);
+                const uint64_t e = pair_of(ex2(d0), ex2(d1));
+                z = pair_add(z, e);
+                w = pair_fma(e, pair_of(d0, d1), w);
+            }
         }
     }
 }
@@ -321,45 +343,60 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobsA
     const int nvec = (a.vocab + skew + N - 1) / N;
     const int v0 = int(int64_t(split) * nvec / a.splits), v1 = int(int64_t(split + 1) * nvec / a.splits);
     const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u; // -inf
-    // a vector, -inf where there is no token
+    // any vector, -inf where the row has no token
     auto load = [&](int v) {
         const int t0 = v * N - skew;
-        uint4 raw = make_uint4(none, none, none, none);
-        if (v < v1) {
-            if (t0 >= 0 && t0 + N <= a.vocab) {
-                raw = ld_once(x + t0);
-            } else {
-                float f[N];
+        if (t0 >= 0 && t0 + N <= a.vocab)
+            return ld_once(x + t0);
+        float f[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    f[i] = t0 + i >= 0 && t0 + i < a.vocab ? Vec<T>::one(x, t0 + i) : -CUDART_INF_F;
-                raw = Vec<T>::pack(f);
-            }
-        }
-        return raw;
+        for (int i = 0; i < N; ++i)
+            f[i] = t0 + i >= 0 && t0 + i < a.vocab ? Vec<T>::one(x, t0 + i) : -CUDART_INF_F;
+        return Vec<T>::pack(f);
     };
     Stat s{kLowest, 0.0f, 0.0f};
     uint64_t z = pair_of(0.0f, 0.0f), w = z;
     float top_value = CUDART_NAN_F; // the largest read so far; passed by anything at first
-    uint4 raw[kLpAhead];
+    {
+        // the run's vectors that lie inside the row: f0 .. f1 - 1, thread tid
+        // those at v0 + tid, + 256, ..; the next ones are on their way while
+        // these are taken in
+        const int f0 = max(v0, skew ? 1 : 0), f1 = min(v1, (a.vocab + skew) / N);
+        const uint32_t inside = uint32_t(max(f1 - f0, 0));
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(x - skew) + int64_t(v0 + tid) * 16;
+        uint4 raw[kLpAhead];
+        auto fetch = [&](int at) { // at: the first one's place from f0
 #pragma unroll
-    for (int k = 0; k < kLpAhead; ++k)
-        raw[k] = load(v0 + k * kLpThreads + tid);
-    for (int base = v0; base < v1; base += kLpThreads * kLpAhead) {
-        uint4 now[kLpAhead];
+            for (int k = 0; k < kLpAhead; ++k) {
+                raw[k] = make_uint4(none, none, none, none);
+                if (uint32_t(at + k * kLpThreads) < inside)
+                    raw[k] = ld_once(p + k * kLpThreads * 16);
+            }
+            p += kLpAhead * kLpThreads * 16;
+        };
+        int at = v0 + tid - f0;
+        fetch(at);
+        for (; at < int(inside); at += kLpAhead * kLpThreads) {
+            uint4 now[kLpAhead];
 #pragma unroll
-        for (int k = 0; k < kLpAhead; ++k) {
-            now[k] = raw[k];
-            raw[k] = load(base + (kLpAhead + k) * kLpThreads + tid);
+            for (int k = 0; k < kLpAhead; ++k)
+                now[k] = raw[k];
+            fetch(at + kLpAhead * kLpThreads);
+            float hi;
+            take<T>(s, z, w, now, hi);
+            if (kTop && !(hi <= top_value))
+                top_value = hi;
         }
-        float hi[kLpAhead];
-#pragma unroll
-        for (int k = 0; k < kLpAhead; ++k)
-            take<T>(s, z, w, now[k], hi[k]);
-        if constexpr (kTop) {
-            const float most = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-            if (!(most <= top_value))
-                top_value = most;
+        // the vectors that stick out of the row
+        for (int e = 0; e < 2; ++e) {
+            const int v = e ? nvec - 1 : 0;
+            if (v >= v0 && v < v1 && (v < f0 || v >= f1) && (e == 0 || nvec > 1) && (v - v0) % kLpThreads == tid) {
+                const uint4 edge[1] = {load(v)};
+                float hi;
+                take<T>(s, z, w, edge, hi);
+                if (kTop && !(hi <= top_value))
+                    top_value = hi;
+            }
         }
     }
     {
