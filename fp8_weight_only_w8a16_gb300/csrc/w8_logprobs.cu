@@ -465,19 +465,34 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobsA
         __syncthreads();
         const int per = (nv + kLpThreads - 1) / kLpThreads, pairs = sel.passing * per;
         select_top(sel, a.top, tid, [&](auto &&offer) {
-            for (int i = tid; i < pairs; i += kLpThreads) {
-                const int j = i / per, v = v0 + (i - j * per) * kLpThreads + sel.thread[j], t0 = v * N - skew;
-                if (v < v1) {
-                    const uint4 u[1] = {load(v)};
+            const float least = value_of(uint32_t(sel.bound >> 32));
+            for (int i0 = tid; i0 < pairs; i0 += kLpAhead * kLpThreads) {
+                uint4 u[kLpAhead][1]; // all on their way before the first is looked at
+                int t0[kLpAhead];
+#pragma unroll
+                for (int q = 0; q < kLpAhead; ++q) {
+                    const int i = i0 + q * kLpThreads, j = i / per;
+                    u[q][0] = make_uint4(none, none, none, none);
+                    t0[q] = a.vocab;
+                    if (i < pairs) {
+                        const int v = v0 + (i - j * per) * kLpThreads + sel.thread[j];
+                        if (v < v1) {
+                            u[q][0] = load(v);
+                            t0[q] = v * N - skew;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kLpAhead; ++q) {
                     float lo, hi, f[N];
-                    Vec<T>::range(lo, hi, u);
-                    if (hi < value_of(uint32_t(bound >> 32)))
+                    Vec<T>::range(lo, hi, u[q]);
+                    if (hi < least)
                         continue;
-                    Vec<T>::widen(f, u[0]);
+                    Vec<T>::widen(f, u[q][0]);
 #pragma unroll
                     for (int e = 0; e < N; ++e)
-                        if (t0 + e >= 0 && t0 + e < a.vocab)
-                            offer(key_of(f[e], t0 + e));
+                        if (t0[q] + e >= 0 && t0[q] + e < a.vocab)
+                            offer(key_of(f[e], t0[q] + e));
                 }
             }
         });
