@@ -462,7 +462,8 @@ template <int DN, int DV>
 cudaError_t launch(const w8_latent_expanded &a, cudaStream_t s)
 {
     auto *fn = &expanded_kernel<DN, DV>;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> raised{0};
+    cudaError_t e = raise_smem(raised, reinterpret_cast<const void *>(fn), kSmem);
     if (e != cudaSuccess)
         return e;
     Maps maps;

@@ -967,8 +967,8 @@ cudaError_t launch_latent_paged(const w8_latent_paged &a, void *ws, int sms, cud
 {
     if (sms > kMaxCtas)
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&paged_kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> raised{0};
+    cudaError_t e = raise_smem(raised, reinterpret_cast<const void *>(&paged_kernel), kSmem);
     if (e != cudaSuccess)
         return e;
     alignas(64) CUtensorMap map;

@@ -195,9 +195,9 @@ cudaError_t launch_block_tables(const TableArgs &a, int sms, cudaStream_t s)
 {
     const size_t smem = (3 * size_t(a.n_req) + 1) * sizeof(int32_t);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&block_tables_kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (3 * W8_MAX_REQUESTS + 1) * int(sizeof(int32_t)));
+        static std::atomic<uint64_t> raised{0};
+        const cudaError_t e = raise_smem(raised, reinterpret_cast<const void *>(&block_tables_kernel),
+                                         (3 * W8_MAX_REQUESTS + 1) * int(sizeof(int32_t)));
         if (e != cudaSuccess)
             return e;
     }

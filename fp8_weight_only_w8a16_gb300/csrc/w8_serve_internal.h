@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "w8_serve.h"
 
 namespace w8 {
@@ -59,6 +61,20 @@ cudaError_t launch_logprobs(const LogprobsArgs &a, bool bf16, cudaStream_t s);
 // wait gave up.
 cudaError_t paged_status(int *out, bool reset);
 cudaError_t expanded_status(int *out, bool reset);
+
+// Raise a kernel's dynamic shared-memory limit, once a device (`done`: a bit a
+// device; devices past 63 raise it every time).
+inline cudaError_t raise_smem(std::atomic<uint64_t> &done, const void *fn, int bytes)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)))
+        return e;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return e;
+}
 
 // Launch with the programmatic-dependency attribute (the kernel waits for the
 // stream's previous kernel itself, before its first global access).

@@ -16,7 +16,7 @@ import struct
 import torch
 
 from . import w8
-from .w8 import W8Error, _stream_ptr
+from .w8 import W8Error
 
 LATENT_DIM, LATENT_ROPE, LATENT_ROW = 512, 64, 576
 MAX_REQUESTS, MAX_LATENT_HEADS, MAX_TOP = 16384, 256, 32
@@ -86,6 +86,19 @@ def device_status(reset: bool = False) -> int:
     return int(out.value)
 
 
+# the current stream's handle without a Stream object around it (0.3 us
+# instead of 3), where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _ints(t: torch.Tensor, dtype: torch.dtype = torch.int32, n: int | None = None) -> int:
     assert t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() >= n)
     return t.data_ptr()
@@ -93,8 +106,9 @@ def _ints(t: torch.Tensor, dtype: torch.dtype = torch.int32, n: int | None = Non
 
 def _rows(t: torch.Tensor, cols: int) -> tuple[int, int]:
     """Pointer and row stride of a 2-D bf16 operand."""
-    assert t.dim() == 2 and t.shape[1] == cols and t.stride(1) == 1 and t.element_size() == 2
-    return t.data_ptr(), t.stride(0)
+    row, one = t.stride()
+    assert t.shape[1] == cols and one == 1 and t.element_size() == 2
+    return t.data_ptr(), row
 
 
 def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int, int]:
@@ -107,10 +121,9 @@ def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int,
 
 
 def _cache_fields(cache: torch.Tensor) -> tuple:
-    assert cache.dim() == 3 and cache.shape[2] == LATENT_ROW and cache.element_size() == 2
     page, tok, one = cache.stride()
-    assert one == 1
-    n, size, _ = cache.shape
+    n, size, cols = cache.shape
+    assert cols == LATENT_ROW and one == 1 and cache.element_size() == 2
     tok = tok if size > 1 else max(tok, LATENT_ROW)
     return cache.data_ptr(), page if n > 1 else max(page, size * tok), tok, n, size
 
@@ -140,7 +153,7 @@ def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_size: int,
         _ints(free_head, n=1), block_table.data_ptr(), max(block_table.stride(0), width), width,
         _ints(seq_lens, n=n), _ints(cu_new, n=n + 1), _ints(slots, torch.int64),
         _ints(positions, n=toks), toks, _ints(free_head_out, n=1), _ints(status, n=1),
-        _stream_ptr(stream)))
+        _stream(stream)))
 
 
 def latent_cache_write(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor,
@@ -152,7 +165,7 @@ def latent_cache_write(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Te
     rp, rld = _rows(rope, LATENT_ROPE)
     assert latent.shape[0] >= n and rope.shape[0] >= n
     _check(lib.w8_latent_cache_write(lp, lld, rp, rld, _ints(slots, torch.int64), n,
-                                     _CACHE.pack(*_cache_fields(cache)), _stream_ptr(stream)))
+                                     _CACHE.pack(*_cache_fields(cache)), _stream(stream)))
     return cache
 
 
@@ -186,7 +199,7 @@ def latent_attn_paged(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: torch.Te
         _ints(seq_lens), _ints(cu_q, n=n + 1), *_heads(out, toks, heads, LATENT_DIM),
         _ints(lse, torch.float32, toks * heads) if lse is not None else 0,
         width, n, toks, heads, scale)
-    _check(lib.w8_latent_attn_paged(args, *_workspace(workspace), _stream_ptr(stream)))
+    _check(lib.w8_latent_attn_paged(args, *_workspace(workspace), _stream(stream)))
     return out
 
 
@@ -204,7 +217,7 @@ def latent_attn_expanded(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: tor
         _ints(cu_q), _ints(cu_k, n=n + 1), *_heads(out, toks, heads, d_v),
         _ints(lse, torch.float32, toks * heads) if lse is not None else 0,
         n, toks, n_k, heads, d_nope, d_v, 1 if causal else 0, scale)
-    _check(lib.w8_latent_attn_expanded(args, _stream_ptr(stream)))
+    _check(lib.w8_latent_attn_expanded(args, _stream(stream)))
     return out
 
 
@@ -238,5 +251,5 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprob: torch.Te
         _ints(tokens, n=rows), _ints(logprob, torch.float32, rows),
         _ints(entropy, torch.float32, rows) if entropy is not None else None, top,
         _ints(top_ids) if top else None, _ints(top_logprobs, torch.float32) if top else None,
-        *_workspace(workspace), _stream_ptr(stream)))
+        *_workspace(workspace), _stream(stream)))
     return logprob
