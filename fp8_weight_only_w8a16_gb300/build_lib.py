@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libw8.so")
 
 SOURCES = ["w8_api.cu", "w8_gemv.cu", "w8_tc.cu", "w8_repack.cu", "w8_noalloc.cu",
            "w8_serve_api.cu", "w8_paging.cu", "w8_latent_paged.cu", "w8_latent_expanded.cu",
-           "w8_logprobs.cu"]
+           "w8_latent_pair.cu", "w8_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "-Xptxas", "-v", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -1,12 +1,9 @@
 // w8_latent_expanded.cu -- latent attention, expanded form, over the keys and
 // values of a prompt (w8_latent_attn_expanded).
 //
-// With s = scale log2 e and a running reference m_i of query i,
-//   x_ij = q_i . k_j,  p_ij = 2^(s x_ij - m_i),  z_i = sum_j p_ij,
-//   out_i = sum_j p_ij v_j / z_i,  lse_i = (m_i + log2 z_i) ln 2.
-// A CTA takes 128 queries of one head and walks over the keys they see, 128 at
-// a time.  Both products run on tcgen05 with fp32 accumulators in tensor
-// memory:
+// The kernel for few queries (mathematics and softmax: w8_expanded.cuh; many
+// take pairs of CTAs, w8_latent_pair.cu).  A CTA takes 128 queries of one head.
+// Both products run on tcgen05 with fp32 accumulators in tensor memory:
 //   S [128 x 128] = Q K^T  (16 or 12 steps of 64 cycles)
 //   O [128 x d_v] += P V   (8 steps of 128 or 64 cycles), P as bf16 in tensor
 //     memory, in the columns of the S that it was made from.
@@ -21,18 +18,7 @@
 // columns, K-major; a V slot 64 keys x d_v columns, MN-major.  The parts of a
 // head's key (its own columns, the rope columns all heads share) meet only in
 // shared memory.
-//
-// The reference moves only when a row's maximum passes it by 2^8: the weights
-// are made against the reference as it stands, and a pair of warps redoes them
-// (and rescales its rows of O) when one of its rows has passed it.
-#include <cuda.h>
-#include <cuda_runtime.h>
-#include <math_constants.h>
-#include <stdint.h>
-
-#include "w8_device.cuh"
-#include "w8_serve_internal.h"
-#include "w8_tcgen.cuh"
+#include "w8_expanded.cuh"
 
 namespace w8 {
 
@@ -40,15 +26,7 @@ __device__ int g_expanded_status;
 
 namespace {
 
-using namespace tcg;
-
-constexpr int kRows = 128, kKeys = 128;       // queries of a CTA, keys of a tile
-constexpr int kSoftWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
-constexpr int kExpThreads = 320;
-constexpr int kSmem = 227 * 1024 - 2048;
-constexpr int kTmemCols = 512;
-constexpr float kRaise = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+using namespace expanded;
 
 template <int DN, int DV>
 struct Shape {
@@ -70,13 +48,9 @@ struct Shared {
     int count[kExpThreads / 32];
     int found[6];
     uint32_t tmem;
-    float top[2][kRows], z[kRows];
+    float top[4][2][32];
 };
 static_assert(sizeof(Shared) <= 2048, "shared memory");
-
-struct Maps {
-    CUtensorMap q_nope, q_rope, k_nope, k_rope, v;
-};
 
 // What a CTA works on.
 struct Item {
@@ -85,13 +59,6 @@ struct Item {
     int see0;       // keys that the first query sees, uncut; one more for each later one (causal)
     int tiles;      // key tiles; 0: nothing is seen
 };
-
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 
 template <int DN, int DV>
 __global__ void __launch_bounds__(kExpThreads, 1)
@@ -321,67 +288,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         auto wait = [&](uint64_t *bar, int ph) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, uint32_t(ph & 1))); };
         float m = -CUDART_INF_F, z = 0.0f;
         for (int t = 0; t < it.tiles; ++t) {
-            const int j0 = t * kKeys + 64 * half;
-            const uint32_t col = tm_s + lanes + uint32_t((t & 1) * kKeys + 64 * half);
             wait(&sh.s[t & 1], t >> 1);
             fence_after();
-            float x[64];
-            ld32x32(&x[0], col);
-            ld32x32(&x[32], col + 32);
-            wait_ld();
-            if (j0 + 64 > lim) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (j0 + i >= lim)
-                        x[i] = -CUDART_INF_F;
-            }
-            float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i < 64; ++i)
-                top[i & 3] = fmaxf(top[i & 3], x[i]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl;
-            // -inf + 8 is -inf: the first key that is seen raises it
-            if (sync_any(1 + quarter, 64, t == 0 || mx > m + kRaise)) {
-                sh.top[half][row] = mx;
-                sync_some(1 + quarter, 64);
-                const float all = fmaxf(mx, sh.top[half ^ 1][row]);
-                float f = 1.0f;
-                if (t == 0) {
-                    m = all;
-                } else if (all > m + kRaise) {
-                    f = ex2(m - all); // 0 from -inf: nothing is summed yet
-                    m = all;
-                    z *= f;
-                }
-                if (t > 0) {
-                    wait(&sh.o, t - 1);
-                    fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < DV / 2; c += 32) {
-                        float o[32];
-                        ld32x32(o, tmem + lanes + uint32_t(DV / 2 * half + c));
-                        wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] *= f;
-                        st32x32(tmem + lanes + uint32_t(DV / 2 * half + c), o);
-                    }
-                    wait_st();
-                }
-                sync_some(1 + quarter, 64); // sh.top is read
-            }
-            const float ref = m == -CUDART_INF_F ? 0.0f : m;
-            float sum[4] = {};
-            uint32_t p[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float e0 = ex2(fmaf(x[2 * i], sl, -ref)), e1 = ex2(fmaf(x[2 * i + 1], sl, -ref));
-                sum[i & 3] += e0 + e1;
-                p[i] = pack_bf16(e0, e1);
-            }
-            z += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            st32x32u(col, p); // over this thread's own scores
-            wait_st();
+            softmax_half<DV>(tm_s + lanes + uint32_t((t & 1) * kKeys + 64 * half), tmem + lanes, t * kKeys + 64 * half, lim, sl,
+                             t == 0, quarter, half, lane, sh.top[quarter], m, z, [&] { wait(&sh.o, t - 1); });
             if (t == it.tiles - 1 && it.nk < it.tiles * kKeys) {
                 // values past the request's keys may be anything: their weights are 0, 0 x NaN is not
                 const int first = it.nk - t * kKeys, slot0 = it.tiles * S::kKSlots + t * S::kVSlots;
@@ -395,47 +305,38 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 }
                 fence_async_shared();
             }
+            // (waited for before this tile's output can be made, so that the
+            // barrier is never two uses ahead of a warp)
+            if (t > 0)
+                wait(&sh.o, t - 1);
             fence_before();
             bar_arrive(&sh.p[t & 1]);
         }
-        // one use after the other: of the last two, either may be open still
-        if (it.tiles > 1)
-            wait(&sh.o, it.tiles - 2);
         if (it.tiles > 0)
             wait(&sh.o, it.tiles - 1);
         fence_after();
-        if (half == 1)
-            sh.z[row] = z;
-        else
-            sh.top[0][row] = z;
+        sh.top[quarter][half][lane] = z;
         sync_some(1 + quarter, 64);
-        z = sh.top[0][row] + sh.z[row];
+        z = sh.top[quarter][0][lane] + sh.top[quarter][1][lane];
         const bool some = z > 0.0f || z != z;
         const float inv = some ? 1.0f / z : 0.0f;
-        const int64_t tok = it.q0 + row;
         if (row < it.rows && half == 0 && a.lse)
-            a.lse[tok * a.n_heads + head] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
-        uint16_t *out = a.out + tok * a.ld_out_tok + head * a.ld_out_head + DV / 2 * half;
-#pragma unroll 1
-        for (int c = 0; c < DV / 2; c += 32) {
-            float o[32];
-            if (it.tiles > 0) {
-                ld32x32(o, tmem + lanes + uint32_t(DV / 2 * half + c));
-                wait_ld();
-            }
-            if (row < it.rows) {
+            a.lse[(int64_t(it.q0) + row) * a.n_heads + head] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
+        // The rows go out through shared memory, where Q was (every score is
+        // made), so that a warp stores whole rows: a lane's row straight from
+        // tensor memory took 32 half-used sectors a store, 4 us a CTA.
+        uint8_t *const stage = sm + 32 * quarter * DV * 2; // of this pair of warps
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (it.tiles > 0) {
-                        u.x = pack_bf16(o[8 * v] * inv, o[8 * v + 1] * inv);
-                        u.y = pack_bf16(o[8 * v + 2] * inv, o[8 * v + 3] * inv);
-                        u.z = pack_bf16(o[8 * v + 4] * inv, o[8 * v + 5] * inv);
-                        u.w = pack_bf16(o[8 * v + 6] * inv, o[8 * v + 7] * inv);
-                    }
-                    *reinterpret_cast<uint4 *>(out + c + 8 * v) = u;
-                }
-            }
+        for (int c = 0; c < DV / 2; c += 32)
+            stage32(stage, DV * 2, tmem + lanes + uint32_t(DV / 2 * half + c), it.tiles > 0, inv, (DV / 2 * half + c) / 8, lane);
+        sync_some(1 + quarter, 64);
+        constexpr int kVecs = DV / 8, kAtOnce = 32 / kVecs; // vectors of a row, rows of a store
+#pragma unroll 4
+        for (int r = 16 * half; r < 16 * half + 16; r += kAtOnce) {
+            const int mine = r + lane / kVecs, v = lane % kVecs, i = 32 * quarter + mine;
+            if (i < it.rows)
+                *reinterpret_cast<uint4 *>(a.out + (int64_t(it.q0) + i) * a.ld_out_tok + head * a.ld_out_head + 8 * v) =
+                    *reinterpret_cast<const uint4 *>(stage + mine * DV * 2 + ((v ^ (mine & 7)) << 4));
         }
     }
     if (!ok)
@@ -449,15 +350,6 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     }
 }
 
-// [toks][heads][cols] read in boxes of 64 columns x 1 head x `rows` tokens.
-bool map_heads(CUtensorMap *m, const uint16_t *p, int toks, int heads, int cols, int64_t ld_tok, int64_t ld_head, int rows)
-{
-    const uint64_t sizes[3] = {uint64_t(cols), uint64_t(heads), uint64_t(toks)};
-    const uint64_t strides[2] = {uint64_t(ld_head) * 2, uint64_t(ld_tok) * 2};
-    const uint32_t box[3] = {64, 1, uint32_t(rows)};
-    return encode_bf16_map(m, p, 3, sizes, strides, box);
-}
-
 template <int DN, int DV>
 cudaError_t launch(const w8_latent_expanded &a, cudaStream_t s)
 {
@@ -467,18 +359,7 @@ cudaError_t launch(const w8_latent_expanded &a, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     Maps maps;
-    bool ok = map_heads(&maps.q_nope, a.q_nope, a.n_q, a.n_heads, DN, a.ld_qnope_tok, a.ld_qnope_head, kRows) &&
-              map_heads(&maps.q_rope, a.q_rope, a.n_q, a.n_heads, W8_LATENT_ROPE, a.ld_qrope_tok, a.ld_qrope_head, kRows);
-    if (a.n_k > 0) { // without keys nothing is copied
-        const uint64_t sizes[2] = {W8_LATENT_ROPE, uint64_t(a.n_k)}, strides[1] = {uint64_t(a.ld_krope_tok) * 2};
-        const uint32_t box[2] = {64, kKeys};
-        ok = ok && map_heads(&maps.k_nope, a.k_nope, a.n_k, a.n_heads, DN, a.ld_knope_tok, a.ld_knope_head, kKeys) &&
-             map_heads(&maps.v, a.v, a.n_k, a.n_heads, DV, a.ld_v_tok, a.ld_v_head, 64) &&
-             encode_bf16_map(&maps.k_rope, a.k_rope, 2, sizes, strides, box);
-    } else {
-        maps.k_nope = maps.v = maps.k_rope = maps.q_rope;
-    }
-    if (!ok)
+    if (!map_all(maps, a, kKeys, 64))
         return cudaErrorInvalidValue;
     // query tiles: every request may end in a part of one
     const int64_t tiles = a.n_q / kRows + (a.n_req < a.n_q ? a.n_req : a.n_q);
@@ -489,8 +370,16 @@ cudaError_t launch(const w8_latent_expanded &a, cudaStream_t s)
 
 } // namespace
 
-cudaError_t launch_latent_expanded(const w8_latent_expanded &a, int, cudaStream_t s)
+cudaError_t launch_latent_expanded(const w8_latent_expanded &a, int sms, cudaStream_t s)
 {
+    // Pairs of CTAs halve what comes from L2 and run on from item to item, but
+    // start later and pad queries to 256: they pay from about five waves of
+    // 128-query tiles on, of requests that fill their tiles.  64 heads of
+    // 192 + 64 / 256, one prompt of 4096: 365 us in pairs, 391 by CTAs; of 2048:
+    // 121 and 127; of 1024: 50.0 and 49.5; 32 requests of 20: 132 and 109; 16
+    // heads, 9 requests of 700: 64 and 69; one of 1024: 25 and 16.
+    if (int64_t(a.n_q) * a.n_heads >= int64_t(5) * kRows * sms && a.n_q / a.n_req >= 512)
+        return launch_expanded_pairs(a, s);
     return a.d_nope == 192 ? launch<192, 256>(a, s) : launch<128, 128>(a, s);
 }
 

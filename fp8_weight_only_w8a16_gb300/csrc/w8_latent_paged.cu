@@ -202,14 +202,6 @@ struct Turn {
     }
 };
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // Keys that the last row of the walk's group sees.
 __device__ __forceinline__ int group_sees(const w8_latent_paged &a, const Walk &w, int nr)
 {

@@ -83,10 +83,11 @@ w8_status w8_serve_device_status(int *status, int reset)
 {
     if (!status)
         return W8_ERR_NULL;
-    int paged = 0, expanded = 0;
-    if (w8::paged_status(&paged, reset != 0) != cudaSuccess || w8::expanded_status(&expanded, reset != 0) != cudaSuccess)
+    int paged = 0, expanded = 0, pairs = 0;
+    if (w8::paged_status(&paged, reset != 0) != cudaSuccess || w8::expanded_status(&expanded, reset != 0) != cudaSuccess ||
+        w8::pairs_status(&pairs, reset != 0) != cudaSuccess)
         return W8_ERR_CUDA;
-    *status = (paged ? 1 : 0) | (expanded ? 2 : 0);
+    *status = (paged ? 1 : 0) | (expanded || pairs ? 2 : 0);
     return W8_OK;
 }
 

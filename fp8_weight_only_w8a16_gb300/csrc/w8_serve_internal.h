@@ -34,6 +34,7 @@ cudaError_t launch_latent_paged(const w8_latent_paged &a, void *ws, int sms, cud
 size_t latent_paged_ws_bytes(int n_tok, int n_heads, int n_req, int sms);
 
 cudaError_t launch_latent_expanded(const w8_latent_expanded &a, int sms, cudaStream_t s);
+cudaError_t launch_expanded_pairs(const w8_latent_expanded &a, cudaStream_t s); // its kernel for pairs of CTAs
 
 // Logits of one row go to `splits` CTAs; their partial results meet in the
 // workspace: a head of kLogprobsCounters arrival counters, one a row, always
@@ -61,6 +62,7 @@ cudaError_t launch_logprobs(const LogprobsArgs &a, bool bf16, cudaStream_t s);
 // wait gave up.
 cudaError_t paged_status(int *out, bool reset);
 cudaError_t expanded_status(int *out, bool reset);
+cudaError_t pairs_status(int *out, bool reset);
 
 // Raise a kernel's dynamic shared-memory limit, once a device (`done`: a bit a
 // device; devices past 63 raise it every time).

@@ -51,6 +51,23 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
     return false;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// ... which one it is, too.  (Steps and copies issued under `lane == 0` take four
+// times as long as under the predicate of the election itself.)
+__device__ __forceinline__ bool elect_one(uint32_t &who)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync %1|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r), "=r"(who));
+    return r != 0;
+}
+
 // Generic-proxy writes to shared memory before this are seen by later
 // tensor-core steps and bulk copies.
 __device__ __forceinline__ void fence_async_shared()

@@ -321,6 +321,59 @@ def test_expanded_chunk_of_a_longer_prompt(serve, nope, v):
     Expanded([129, 40], [1700, 1064], 4, nope, v, seed=6).check(serve)
 
 
+def pairs(serve, c):
+    """Whether the case is long enough for the kernel of CTA pairs."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n_q, n_req = c.cu_q[-1], len(c.cu_q) - 1
+    return n_q * c.heads >= 5 * 128 * sms and n_q // n_req >= 512
+
+
+@pytest.mark.parametrize("nope,v", DIMS)
+@pytest.mark.parametrize("q,k,causal", [
+    ([1600], [1600], True), ([1537], [1700], True), ([520, 1111], [520, 1400], True),
+    ([1, 1900, 0], [200, 1900, 64], True), ([1543], [130], True), ([1550], [1551], False)])
+def test_expanded_long_prompts(serve, nope, v, q, k, causal):
+    """The kernel of CTA pairs: several items a pair, ragged ends, queries that see nothing."""
+    c = Expanded(q, k, 64, nope, v, seed=sum(q), causal=causal)
+    assert pairs(serve, c)
+    first, fl = c.check(serve)
+    for _ in range(3):
+        out, lse = c.run(serve)
+        assert torch.equal(out, first) and torch.equal(lse, fl)
+
+
+@pytest.mark.parametrize("nope,v", DIMS)
+def test_expanded_long_prompts_beside_anything(serve, nope, v):
+    """Other requests' keys may hold anything, rows past a request's queries are not touched, peaks rise all along."""
+    c = Expanded([1100, 530], [1100, 530], 64, nope, v, seed=21, extra=8)
+    assert pairs(serve, c)
+    c.k_rope[:, 0] = torch.arange(1630, device="cuda") / 8
+    c.q_rope[:, :, 0] = 4.0
+    want, wl = c.check(serve)
+    bad = torch.tensor([float("nan"), float("inf"), NEG], device="cuda").to(BF)
+    c.k_nope[1100:], c.v[1100:] = bad.repeat(nope)[:nope], bad.repeat(v)[:v]
+    out, lse = c.run(serve)
+    assert torch.equal(out[:1100], want[:1100]) and torch.equal(lse[:1100], wl[:1100])
+    assert torch.isnan(out[1100:]).any()
+    c = Expanded([1630], [1630], 64, nope, v, seed=22)
+    want, wl = c.run(serve)
+    store = torch.full((1630, 64, v + 24), 3.0, dtype=BF, device="cuda")
+    serve.latent_attn_expanded(c.q_nope, c.q_rope, c.k_nope, c.k_rope, c.v, i32(c.cu_q), i32(c.cu_k), c.scale, True,
+                               store[:, :, 8:8 + v], None)
+    assert torch.equal(store[:, :, 8:8 + v], want)
+    assert (store[:, :, :8] == 3).all() and (store[:, :, 8 + v:] == 3).all()
+    # a graph replayed behind other work of the stream
+    out, lse = torch.zeros_like(want), torch.zeros_like(wl)
+    cq, ck = i32(c.cu_q), i32(c.cu_k)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            serve.latent_attn_expanded(c.q_nope, c.q_rope, c.k_nope, c.k_rope, c.v, cq, ck, c.scale, True, out, lse)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 @pytest.mark.parametrize("nope,v", DIMS)
 def test_expanded_many_heads(serve, nope, v):
     Expanded([300, 65], [300, 80], 64, nope, v, seed=7).check(serve)
