@@ -23,12 +23,14 @@
 // MN-major for the second.  Rows of Q past the group read whatever follows
 // in shared memory: they make rows of S that nobody reads.
 //
-// Seven warps: 0-3 softmax (16 rows each; loads S, writes P as bf16 into shared
-// memory, raises the reference, divides and stores), 4 copies (tensor-map
-// boxes of min(page, 64) tokens x 64 columns), 5 and 6 issue the two products
-// (a warp each, so that a tile's second product does not wait for the next
-// tile's copies).  Two tiles are in flight, each in two halves: columns
+// Eleven warps: 0-7 softmax and output (16 rows a warp, half the tile's tokens;
+// S is read, the weights made against the reference as it stands, stored as bf16
+// in shared memory, and redone when some row has passed its reference), 8 copies
+// (tensor-map boxes of min(page, 64) tokens x 64 columns), 9 and 10 issue the two
+// products (a warp each, so that a tile's second product does not wait for the
+// next tile's copies).  Two tiles are in flight, each in two halves: columns
 // 0 .. 255, freed when the second product has passed over them, and the rest.
+// The next group's queries are loaded while this one's output is stored.
 // The reference moves only when a row's maximum passes it by 2^8 (p stays
 // below 2^8, and 2^8 of fp32's range costs no precision): O is then rescaled
 // in tensor memory, for most inputs once or twice in the first tiles.
