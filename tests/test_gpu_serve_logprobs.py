@@ -11,7 +11,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests.serve_util import U, logprobs64
+from tests.serve_util import NEG, U, logprobs64
 
 pytestmark = pytest.mark.gpu
 REL = 2.0 ** -20 + 2048 * U
@@ -111,6 +111,24 @@ def check_lowest(serve, y, tok):
     assert torch.equal(ids.long(), wids)
     assert torch.allclose(lp.double(), wlp, rtol=2.0 ** -19, atol=2e-4)
     assert torch.allclose(ent.double(), went, rtol=0, atol=2e-3)
+
+
+@pytest.mark.parametrize("top", [1, 20, 32])
+@pytest.mark.parametrize("kept", [0, 5, 400])
+def test_masks_in_every_place(serve, kept, top):
+    """Few tokens above a value that the rest share -- -inf, the lowest, or any other --
+    and the shared value's own lowest tokens behind them."""
+    g = torch.Generator().manual_seed(kept + top)
+    for fill in (NEG, -3.0e38, -1.0, 2.0):
+        x = torch.full((3, 60013), fill)
+        for r in range(3):
+            at = torch.randperm(60013, generator=g)[:kept]
+            x[r, at] = torch.rand(kept, generator=g) * 3 + 2.5
+        x[1, :30000] = min(fill, -2.0) * 1.1 if fill > NEG else NEG  # the shared value starts late
+        x = x.cuda()
+        order = torch.sort(x.double(), dim=1, descending=True, stable=True).indices[:, :top]
+        _, _, ids, _ = run(serve, x, torch.zeros(3, dtype=torch.int32, device="cuda"), top)
+        assert torch.equal(ids.long(), order), fill
 
 
 def test_lowest_value_everywhere(serve):
