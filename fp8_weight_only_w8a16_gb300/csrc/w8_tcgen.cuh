@@ -59,8 +59,8 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// ... which one it is, too.  (Steps and copies issued under `lane == 0` take four
-// times as long as under the predicate of the election itself.)
+// ... which one it is, too.  (Steps are issued under the predicate of the election
+// itself: under `lane == 0` one took 59 cycles to issue instead of 10.)
 __device__ __forceinline__ bool elect_one(uint32_t &who)
 {
     uint32_t r;
