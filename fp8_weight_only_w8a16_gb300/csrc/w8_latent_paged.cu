@@ -36,18 +36,23 @@
 // in tensor memory, for most inputs once or twice in the first tiles.
 //
 // The work is cut by tiles, not by requests: all groups' tiles in one line,
-// an equal run a CTA, one CTA an SM.  A group that more than one run touches
-// leaves its parts (O, m, z in fp32) in the workspace, and a second kernel
-// joins them.  Lengths are read on the device; the line's length picks NR:
-// 64 rows a group, or fewer when there are not enough tiles to give every SM
-// one.
+// an equal run a CTA, one CTA an SM.  A group's begin takes four places of the
+// line too, for its queries' load and its output's store cost a CTA about as
+// much as four tiles (24 requests of 1 to 4 query tokens, 64 heads: 80.3 us
+// with no such place, 75.4 with two, 72.7 with four, 75.6 with eight; 400
+// requests of up to 2000 tokens 140, 126, 118 with none, two, four); cuts that
+// fall there move to the group's first tile, and split no group.  A group that
+// more than one run touches leaves its parts (O, m, z in fp32) in the
+// workspace, and a second kernel joins them.  Lengths are read on the device;
+// the line's length picks NR: 64 rows a group, or fewer when there are not
+// enough tiles to give every SM one.
 //
-// Measured (replayed, 64 heads): 128 requests of up to 16384 tokens 213 us,
-// 5.5 TB/s of HBM in the first kernel, 3000 cycles a tile where its bytes alone
-// take 3140 at the copy rate's share of an SM at 1.9 GHz; 24 requests of 1 to 4
-// query tokens over up to 8111 tokens 81 us, bound by the chain copy - scores -
-// softmax - output with two tiles in flight (tensor pipe 31 %); one request of
-// 1531 tokens 15 us, latency.
+// Measured (replayed, 64 heads): 128 requests of up to 16384 tokens 202 us,
+// 5.8 TB/s of HBM in the first kernel, about the rate of a copy; 24 requests of
+// 1 to 4 query tokens over up to 8111 tokens 73 us, bound by the chain copy -
+// scores - softmax - output with two tiles in flight (2900 cycles a tile, the
+// tensor cores' share 1920) and by the parts (26 MB written and read back); one
+// request of 1531 tokens 13 us, latency.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -76,6 +81,7 @@ constexpr int kPagedThreads = 352, kSoftThreads = 256, kCopyWarp = 8, kScoreWarp
 constexpr int kMaxSlots = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
+constexpr int kBegin = 4;                    // places of a group's begin in the line
 constexpr float kRaise = 8.0f;               // log2 of how far a row's weights may pass 1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -102,11 +108,11 @@ static_assert(smem_plan(64).end <= kSmem - 1024 && smem_plan(32).end <= kSmem - 
 static_assert(smem_plan(16).end >= 8 * 16 * 128 + kChunk, "Q's reach");
 
 // What the parts of split groups need: [2 CTAs][64][512] fp32, [2 CTAs][64]
-// (m, z), [CTAs] the group that runs over the CTA's start.
+// (m, z), [CTAs] the group that runs over the CTA's start, if it runs over no
+// earlier CTA's.
 struct Boundary {
-    int first, last; // CTAs that hold the group's parts; last < 0: none starts before this CTA
+    int first, last; // CTAs that hold the group's parts; last < 0: this CTA's start is no group's first crossed one
     int row0, rows;  // the group's rows, counted over all query tokens' heads
-    int first_slot;  // the first CTA's part
 };
 struct Parts {
     float *o;
@@ -153,10 +159,10 @@ __device__ __forceinline__ int group_tiles(const Request &q, int heads, int nr, 
 }
 __device__ __forceinline__ int groups_of(const Request &q, int heads, int nr) { return (q.q * heads + nr - 1) / nr; }
 
-// One CTA's place in the line of tiles, a run of one group at a time.  Every
-// role walks it for itself.
+// One CTA's place in the line, a run of one group at a time.  Every role walks
+// it for itself.  A group takes kBegin places and one for each of its tiles.
 struct Walk {
-    int64_t pos, end;  // the next tile, the CTA's last + 1
+    int64_t pos, end;  // the next tile's place, the CTA's last + 1
     int r, g, off;     // its request, group, place in the group
     Request req;
     int tiles;         // of the group
@@ -165,7 +171,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const w8_latent_paged &a, int nr, bool first)
     {
         if (!first) {
-            pos += run;
+            pos += run + kBegin;
             off = 0;
             if (pos < end && ++g >= groups_of(req, a.n_heads, nr)) {
                 g = 0;
@@ -191,7 +197,7 @@ struct Shared {
     int64_t out[kMaxRows]; // a row's place in the output
     int64_t sum[kPagedThreads / 32];
     int max[kPagedThreads / 32], few[kPagedThreads / 32];
-    int start[3];
+    int start[4];
     uint32_t tmem;
     float f[kMaxRows], top[2][kMaxRows];
 };
@@ -644,13 +650,14 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
         }
         if (w.off > 0 && tid == 0) {
             // the group runs over this CTA's start
-            const int64_t s0 = w.pos - w.off, s1 = s0 + w.tiles - 1; // the group's tiles in the line
+            const int64_t s0 = w.pos - w.off, s1 = s0 + w.tiles - 1; // the group's tiles' places
             Boundary b;
             b.first = int(((s0 + 1) * ctas - 1) / total);
             b.last = int(((s1 + 1) * ctas - 1) / total);
             b.row0 = w.req.q0 * a.n_heads + row0;
             b.rows = rows;
-            b.first_slot = 2 * b.first + 1;
+            if (b.first != int(blockIdx.x) - 1)
+                b.last = -1; // an earlier start names the group
             parts.at[blockIdx.x] = b;
         }
         if (vis > 0)
@@ -735,12 +742,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     Request held{0, 0, 0}; // the thread's first request, mostly its only one
     if (r0 < r1)
         held = request_of(a, r0);
-    // this thread's tiles with nr rows a group
-    auto tiles_of = [&](int nr) {
+    // this thread's tiles with nr rows a group, and a group's begin as that of so many
+    auto tiles_of = [&](int nr, int begin) {
         int64_t sum = 0;
         for (int r = r0; r < r1; ++r) {
             const Request q = r == r0 ? held : request_of(a, r);
             const int n = groups_of(q, a.n_heads, nr);
+            sum += int64_t(n) * begin;
             if (q.q == 1) // all groups see the same
                 sum += int64_t(n) * max((q.len + kTile - 1) / kTile, 1);
             else
@@ -749,13 +757,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         return sum;
     };
-    int rows = 0;
-    for (int r = r0; r < r1; ++r)
-        rows = max(rows, min((r == r0 ? held : request_of(a, r)).q * a.n_heads, kMaxRows + 1));
+    int rows = 0, groups64 = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Request q = r == r0 ? held : request_of(a, r);
+        rows = max(rows, min(q.q * a.n_heads, kMaxRows + 1));
+        groups64 += groups_of(q, a.n_heads, 64);
+    }
     // fewer rows a group: when no group would be filled, or when twice as many
     // groups still leave no SM two tiles (a thread's count past 2^16 is many)
     rows = __reduce_max_sync(0xffffffffu, rows);
-    int64_t mine = tiles_of(64);
+    int64_t mine = tiles_of(64, 0);
     const int few = __reduce_add_sync(0xffffffffu, int(min(mine, int64_t(1 << 16))));
     if (lane == 0) {
         sh.max[warp] = rows;
@@ -769,8 +780,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     }
     const int grid = int(gridDim.x), rows_max = rows;
     const int nr = rows > 32 && all64 * 2 > grid ? 64 : rows > 16 && all64 * 4 > grid ? 32 : 16;
-    if (nr != 64)
-        mine = tiles_of(nr);
+    mine = nr != 64 ? tiles_of(nr, kBegin) : mine + int64_t(groups64) * kBegin;
     int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -801,11 +811,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             const Request q = r == r0 ? held : request_of(a, r);
             const int n = groups_of(q, a.n_heads, nr);
             for (int g = 0; g < n; ++g) {
-                const int t = group_tiles(q, a.n_heads, nr, g);
+                const int t = kBegin + group_tiles(q, a.n_heads, nr, g);
                 if (at <= w.pos && w.pos < at + t) {
+                    const int place = int(w.pos - at);
                     sh.start[0] = r;
                     sh.start[1] = g;
-                    sh.start[2] = int(w.pos - at);
+                    sh.start[2] = max(place - kBegin, 0);
+                    sh.start[3] = max(kBegin - place, 0);
                 }
                 at += t;
             }
@@ -815,9 +827,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem, tm_s = tmem + 4 * kMaxRows; // O in columns 0 .., S after it
-    w.r = sh.start[0];
-    w.g = sh.start[1];
-    w.off = sh.start[2];
+    if (w.pos < w.end) { // else nobody has written the start
+        w.r = sh.start[0];
+        w.g = sh.start[1];
+        w.off = sh.start[2];
+        w.pos += sh.start[3]; // past the group's begin; a CTA may have nothing else
+    }
     const Parts parts = parts_of(ws, int(gridDim.x));
     const int role = __shfl_sync(0xffffffffu, warp, 0);
     auto roles = [&](auto rows) {
@@ -842,87 +857,108 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 }
 
 // Joins the parts of the split groups: a block takes one row of one group at
-// a time, a thread four latent columns.  The crossed CTA starts are listed in
-// shared memory first; a group is named by the first start that it crosses.
-constexpr int kJoinThreads = W8_LATENT_DIM / 4, kMaxCtas = 1024;
-__global__ void __launch_bounds__(kJoinThreads)
+// a time, a thread four latent columns.  A group is named by the first CTA
+// start that it crosses; every warp ranks the starts for itself, one lane a
+// start, so that no barrier stands before the loads.  A warp's lanes hold the
+// parts' (m, z), and the first parts' O are on their way while these are
+// reduced.  Six blocks an SM, all resident at once: with twelve the second half
+// starts over with the ranks (one request of 1531 tokens 14.8 us to 13.3).
+constexpr int kJoinThreads = W8_LATENT_DIM / 4, kJoinBlocks = 6, kJoinDeep = 8, kMaxCtas = 1024;
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     join_kernel(const __grid_constant__ w8_latent_paged a, void *ws, int ctas)
 {
-    __shared__ int s_list[kMaxCtas];
-    __shared__ int s_n;
-    __shared__ uint8_t s_yes[kMaxCtas];
-    const int tid = threadIdx.x;
-    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
     const Parts parts = parts_of(ws, ctas);
-    for (int c = 1 + tid; c < ctas; c += kJoinThreads)
-        s_yes[c] = parts.at[c].last >= 0 && parts.at[c].first == c - 1;
-    __syncthreads();
-    if (tid < 32) { // in order: every block has the same list
-        int n = 0;
-        for (int c0 = 1; c0 < ctas; c0 += 32) {
-            const int c = c0 + tid;
-            const bool yes = c < ctas && s_yes[c] != 0;
-            const uint32_t all = __ballot_sync(0xffffffffu, yes);
-            if (yes)
-                s_list[n + __popc(all & ((1u << tid) - 1))] = c;
-            n += __popc(all);
-        }
-        if (tid == 0)
-            s_n = n;
-    }
-    __syncthreads();
-    for (int job = blockIdx.x; job < s_n * kMaxRows; job += gridDim.x) {
-        const Boundary b = parts.at[s_list[job % s_n]];
-        const int row = job / s_n, n = b.last - b.first + 1;
-        if (row >= b.rows)
-            continue;
-        // part i: the first CTA's, then slot 2 c of each later one; eight
-        // parts' loads are in flight at once, and no thread waits for another
-        auto slot = [&](int i) { return size_t(i ? 2 * (b.first + i) : b.first_slot) * kMaxRows + row; };
-        float m = -CUDART_INF_F, z = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            float2 mz[8];
-            float4 v[8];
+    pdl_wait();
+    // the starts are taken 256 at a time: one pass on a GPU of up to 256 SMs
+    constexpr int kStarts = 8, kSlot = kMaxRows * W8_LATENT_DIM / 4;
+    int before = 0, job = blockIdx.x; // groups of the starts before c0
+    for (int c0 = 0; c0 < ctas; c0 += 32 * kStarts) {
+        int rank[kStarts], groups = before;
+        bool yes[kStarts];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                mz[i] = make_float2(-CUDART_INF_F, 0.0f);
-                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i0 + i < n) {
-                    mz[i] = parts.mz[slot(i0 + i)];
-                    v[i] = reinterpret_cast<const float4 *>(parts.o + slot(i0 + i) * W8_LATENT_DIM)[tid];
+        for (int k = 0; k < kStarts; ++k) {
+            const int c = c0 + 32 * k + lane;
+            yes[k] = c >= 1 && c < ctas && parts.at[c].last >= 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kStarts; ++k) {
+            const uint32_t all = __ballot_sync(0xffffffffu, yes[k]);
+            rank[k] = yes[k] ? groups + __popc(all & ((1u << lane) - 1)) : -1;
+            groups += __popc(all);
+        }
+        for (; job < groups * kMaxRows; job += gridDim.x) {
+            const int row = job % kMaxRows;
+            int at = 0;
+#pragma unroll
+            for (int k = 0; k < kStarts; ++k)
+                at = rank[k] == job / kMaxRows ? c0 + 32 * k + lane : at;
+            const Boundary b = parts.at[__reduce_max_sync(0xffffffffu, at)];
+            if (row >= b.rows)
+                continue;
+            // part i lies in slot 2 (first + i), the first in the one after
+            const int n = b.last - b.first + 1;
+            const float2 *mz = parts.mz + 2 * b.first * kMaxRows + row;
+            const float4 *from = reinterpret_cast<const float4 *>(parts.o) + size_t(2 * b.first) * kSlot + row * (W8_LATENT_DIM / 4) + tid;
+            float m = -CUDART_INF_F, z = 0.0f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const int here = min(n - i0, 32);
+                float2 part = make_float2(-CUDART_INF_F, 0.0f);
+                if (lane < here)
+                    part = mz[(2 * (i0 + lane) + (i0 + lane == 0)) * kMaxRows];
+                float4 v[kJoinDeep];
+                auto load = [&](int j) {
+#pragma unroll
+                    for (int i = 0; i < kJoinDeep; ++i)
+                        if (j + i < here)
+                            v[i] = from[size_t(2 * (i0 + j + i) + (i0 + j + i == 0)) * kSlot];
+                };
+                load(0);
+                float top = part.x;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = fmaxf(top, m);
+                const float ref = top == -CUDART_INF_F ? 0.0f : top;
+                const float f0 = ex2(m - ref), e = ex2(part.x - ref); // 0 for a part that has seen nothing (its O is 0)
+                m = top;
+                float sum = part.y * e;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                z = fmaf(z, f0, sum);
+                o.x *= f0;
+                o.y *= f0;
+                o.z *= f0;
+                o.w *= f0;
+#pragma unroll 1
+                for (int j = 0; j < here; j += kJoinDeep) {
+                    if (j > 0)
+                        load(j);
+#pragma unroll
+                    for (int i = 0; i < kJoinDeep; ++i) {
+                        const float f = __shfl_sync(0xffffffffu, e, j + i);
+                        if (j + i < here) {
+                            o.x = fmaf(v[i].x, f, o.x);
+                            o.y = fmaf(v[i].y, f, o.y);
+                            o.z = fmaf(v[i].z, f, o.z);
+                            o.w = fmaf(v[i].w, f, o.w);
+                        }
+                    }
                 }
             }
-            float top = m;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                top = fmaxf(top, mz[i].x);
-            const float ref = top == -CUDART_INF_F ? 0.0f : top;
-            const float f0 = ex2(m - ref);
-            m = top;
-            z *= f0;
-            o.x *= f0;
-            o.y *= f0;
-            o.z *= f0;
-            o.w *= f0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = ex2(mz[i].x - ref); // 0 for a part that has seen nothing (its O is 0)
-                z = fmaf(mz[i].y, f, z);
-                o.x = fmaf(v[i].x, f, o.x);
-                o.y = fmaf(v[i].y, f, o.y);
-                o.z = fmaf(v[i].z, f, o.z);
-                o.w = fmaf(v[i].w, f, o.w);
-            }
+            const bool some = z > 0.0f || z != z;
+            const float inv = some ? 1.0f / z : 0.0f;
+            const int tok = (b.row0 + row) / a.n_heads, head = b.row0 + row - tok * a.n_heads;
+            uint32_t *out = reinterpret_cast<uint32_t *>(a.out + tok * a.ld_out_tok + head * a.ld_out_head) + 2 * tid;
+            out[0] = pack_bf16(o.x * inv, o.y * inv);
+            out[1] = pack_bf16(o.z * inv, o.w * inv);
+            if (a.lse && tid == 0)
+                a.lse[b.row0 + row] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
         }
-        const bool some = z > 0.0f || z != z;
-        const float inv = some ? 1.0f / z : 0.0f;
-        const int tok = (b.row0 + row) / a.n_heads, head = (b.row0 + row) % a.n_heads;
-        uint32_t *out = reinterpret_cast<uint32_t *>(a.out + tok * a.ld_out_tok + head * a.ld_out_head) + 2 * tid;
-        out[0] = pack_bf16(o.x * inv, o.y * inv);
-        out[1] = pack_bf16(o.z * inv, o.w * inv);
-        if (a.lse && tid == 0)
-            a.lse[b.row0 + row] = some ? (m + log2f(z)) * kLn2 : -CUDART_INF_F;
+        before = groups;
     }
 }
 
@@ -981,7 +1017,7 @@ cudaError_t launch_latent_paged(const w8_latent_paged &a, void *ws, int sms, cud
     e = launch_dependent(&paged_kernel, dim3(unsigned(sms)), kPagedThreads, kSmem, s, a, map, ws);
     if (e != cudaSuccess || sms < 2)
         return e;
-    return launch_dependent(&join_kernel, dim3(unsigned(12 * sms)), kJoinThreads, 0, s, a, ws, sms);
+    return launch_dependent(&join_kernel, dim3(unsigned(kJoinBlocks * sms)), kJoinThreads, 0, s, a, ws, sms);
 }
 
 cudaError_t paged_status(int *out, bool reset)
