@@ -23,14 +23,15 @@
 // MN-major for the second.  Rows of Q past the group read whatever follows
 // in shared memory: they make rows of S that nobody reads.
 //
-// Eleven warps: 0-7 softmax and output (16 rows a warp, half the tile's tokens;
+// Twelve warps: 0-7 softmax and output (16 rows a warp, half the tile's tokens;
 // S is read, the weights made against the reference as it stands, stored as bf16
 // in shared memory, and redone when some row has passed its reference), 8 copies
 // (tensor-map boxes of min(page, 64) tokens x 64 columns), 9 and 10 issue the two
 // products (a warp each, so that a tile's second product does not wait for the
-// next tile's copies).  Two tiles are in flight, each in two halves: columns
+// next tile's copies), 11 loads the queries.  Two tiles are in flight, each in two halves: columns
 // 0 .. 255, freed when the second product has passed over them, and the rest.
-// The next group's queries are loaded while this one's output is stored.
+// The next group's queries are loaded and scored while this one's output is
+// stored.
 // The reference moves only when a row's maximum passes it by 2^8 (p stays
 // below 2^8, and 2^8 of fp32's range costs no precision): O is then rescaled
 // in tensor memory, for most inputs once or twice in the first tiles.
@@ -77,7 +78,7 @@ constexpr int kTile = 64;                    // tokens
 constexpr int kChunk = kTile * 128;          // bytes of 64 tokens x 64 columns
 constexpr int kFront = 4, kBack = 5;         // chunks of a tile's two halves: columns 0 .. 255, 256 .. 575
 constexpr int kMaxRows = 64;
-constexpr int kPagedThreads = 352, kSoftThreads = 256, kCopyWarp = 8, kScoreWarp = 9, kOutWarp = 10;
+constexpr int kPagedThreads = 384, kSoftThreads = 256, kCopyWarp = 8, kScoreWarp = 9, kOutWarp = 10, kQueryWarp = 11;
 constexpr int kMaxSlots = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
@@ -193,7 +194,7 @@ struct Walk {
 // 2 KB at most: the rest is the rings'.
 struct Shared {
     uint64_t front_full[kMaxSlots], front_free[kMaxSlots], back_full[kMaxSlots], back_free[kMaxSlots];
-    uint64_t q, s[2], s_free[2], p, o, end[2];
+    uint64_t q, q_free, s[2], s_free[2], p, o, end[2];
     int64_t out[kMaxRows]; // a row's place in the output
     int64_t sum[kPagedThreads / 32];
     int max[kPagedThreads / 32], few[kPagedThreads / 32];
@@ -360,6 +361,8 @@ __device__ __forceinline__ bool score_role(const w8_latent_paged &a, Walk w, uin
                     mma_ss(d, dq + uint64_t(((kFront + s / 4) * NR * 128 + (s % 4) * 32) >> 4),
                            db + uint64_t(((s / 4) * kChunk + (s % 4) * 32) >> 4), id, 1);
                 commit(&sh.s[n & 1]);
+                if (t == w.run - 1)
+                    commit(&sh.q_free);
             }
             __syncwarp();
             b.step(lay.backs);
@@ -417,29 +420,49 @@ __device__ __forceinline__ bool out_role(const w8_latent_paged &a, Walk w, uint8
     return bar_wait(&sh.end[1], 0) && ok;
 }
 
-// ---- softmax, output --------------------------------------------------------
-// Q of the walk's run, all copies in flight at once: a warp a row, 72 vectors
-// of 16 bytes; rows past the group's are zeros.
+// ---- queries ----------------------------------------------------------------
+// Q of each run, by a warp of its own: the next run's is on its way while this
+// one's output is stored.  8 lanes take 128 bytes of a row, 4 rows a step; rows
+// past the group's are zeros.
 template <int NR>
-__device__ __forceinline__ void load_q(const w8_latent_paged &a, const Walk &w, uint8_t *q, int warp, int lane)
+__device__ __forceinline__ bool query_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, int lane)
 {
-    const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
+    constexpr Smem lay = smem_plan(NR);
+    const uint32_t q = smem_addr(sm + lay.q);
+    const int v = lane & 7;
+    int runs = 0; // with keys
+    bool ok = true;
+    for (bool first = true; ok && w.next(a, NR, first); first = false) {
+        if (group_sees(a, w, NR) == 0)
+            continue;
+        // the last run's scores are made
+        if (runs > 0)
+            ok = __all_sync(0xffffffffu, bar_wait(&sh.q_free, uint32_t((runs - 1) & 1)));
+        if (!ok)
+            break;
+        ++runs;
+        const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
+        int row = lane >> 3, tok = (row0 + row) / a.n_heads, head = row0 + row - tok * a.n_heads;
 #pragma unroll 2
-    for (int row = warp; row < NR; row += kSoftThreads / 32) {
-        const bool some = row < rows;
-        const int tok = some ? (row0 + row) / a.n_heads : 0, head = some ? row0 + row - tok * a.n_heads : 0;
-        const uint16_t *lat = a.q_lat + (w.req.q0 + tok) * a.ld_qlat_tok + head * a.ld_qlat_head;
-        const uint16_t *rope = a.q_rope + (w.req.q0 + tok) * a.ld_qrope_tok + head * a.ld_qrope_head;
+        for (; row < NR; row += 4) {
+            const bool some = row < rows;
+            const uint16_t *lat = some ? a.q_lat + (w.req.q0 + tok) * a.ld_qlat_tok + head * a.ld_qlat_head + 8 * v : a.q_lat;
+            const uint16_t *rope = some ? a.q_rope + (w.req.q0 + tok) * a.ld_qrope_tok + head * a.ld_qrope_head + 8 * v : a.q_rope;
+            const uint32_t to = q + row * 128 + ((v ^ (row & 7)) << 4);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const int v = 32 * k + lane;
-            if (v < 72)
-                copy16(smem_addr(q + (v >> 3) * NR * 128 + row * 128 + (((v & 7) ^ (row & 7)) << 4)),
-                       v < 64 ? lat + 8 * v : rope + 8 * (v - 64), some);
+            for (int c = 0; c < 9; ++c)
+                copy16(to + c * NR * 128, c < 8 ? lat + 64 * c : rope, some);
+            for (head += 4; head >= a.n_heads; head -= a.n_heads)
+                ++tok;
         }
+        copy16_wait();
+        fence_async_shared();
+        bar_arrive(&sh.q);
     }
+    return ok;
 }
 
+// ---- softmax, output --------------------------------------------------------
 template <int NR>
 __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, uint32_t tmem,
                                              uint32_t tm_s, const Parts &parts, int64_t total, int64_t ctas, int tid)
@@ -460,20 +483,9 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
     if (tid == 0 && (w.pos >= w.end || w.off == 0))
         parts.at[blockIdx.x].last = -1; // no group runs over this CTA's start
     int n = 0; // tiles so far
-    bool loaded = false;
     for (bool have = w.next(a, NR, true); have;) {
         const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
         const int vis = seen(w.req, (row0 + rows - 1) / a.n_heads);
-        if (vis > 0 && !loaded) {
-            load_q<NR>(a, w, sm + lay.q, warp, lane);
-            copy16_wait();
-            fence_async_shared();
-            bar_arrive(&sh.q);
-        }
-        loaded = false;
-        Walk nx = w;
-        const bool more = nx.next(a, NR, false);
-        const bool ahead = more && group_sees(a, nx, NR) > 0; // the next run's Q is loaded as soon as this one's is read
         // how many keys this thread's rows see
         int lim[2];
 #pragma unroll
@@ -483,7 +495,24 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
             const int tok = (row0 + tid) / a.n_heads, head = row0 + tid - tok * a.n_heads;
             sh.out[tid] = (w.req.q0 + tok) * a.ld_out_tok + head * a.ld_out_head;
         }
+        if (w.off > 0 && tid == 0) {
+            // the group runs over this CTA's start
+            const int64_t s0 = w.pos - w.off, s1 = s0 + w.tiles - 1; // the group's tiles' places
+            Boundary b;
+            b.first = int(((s0 + 1) * ctas - 1) / total);
+            b.last = int(((s1 + 1) * ctas - 1) / total);
+            b.row0 = w.req.q0 * a.n_heads + row0;
+            b.rows = rows;
+            if (b.first != int(blockIdx.x) - 1)
+                b.last = -1; // an earlier start names the group
+            parts.at[blockIdx.x] = b;
+        }
+        // the run after this one, looked up while the first tile's output is summed
+        Walk nx = w;
+        bool more = false;
         float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, z[2] = {0.0f, 0.0f};
+        if (vis == 0)
+            more = nx.next(a, NR, false);
         if (vis > 0) {
             for (int t = 0; t < w.run; ++t, ++n) {
                 const int j0 = (w.off + t) * kTile, c0 = j0 + 32 * half; // tile's, thread's first token
@@ -496,8 +525,6 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                 }
                 fence_before();
                 bar_arrive(&sh.s_free[n & 1]);
-                if (ahead && t == w.run - 1)
-                    load_q<NR>(a, nx, sm + lay.q, warp, lane);
                 // Weights against the reference as it stands; whether any row has
                 // passed it is asked afterwards, so that no exponential waits
                 // for a maximum.
@@ -614,12 +641,8 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                 fence_before();
                 fence_async_shared();
                 bar_arrive(&sh.p);
-            }
-            if (ahead) {
-                copy16_wait();
-                fence_async_shared();
-                bar_arrive(&sh.q);
-                loaded = true;
+                if (t == 0)
+                    more = nx.next(a, NR, false);
             }
         }
         // ---- the run's result: the output, or a part of it
@@ -648,18 +671,6 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                 }
             }
         }
-        if (w.off > 0 && tid == 0) {
-            // the group runs over this CTA's start
-            const int64_t s0 = w.pos - w.off, s1 = s0 + w.tiles - 1; // the group's tiles' places
-            Boundary b;
-            b.first = int(((s0 + 1) * ctas - 1) / total);
-            b.last = int(((s1 + 1) * ctas - 1) / total);
-            b.row0 = w.req.q0 * a.n_heads + row0;
-            b.rows = rows;
-            if (b.first != int(blockIdx.x) - 1)
-                b.last = -1; // an earlier start names the group
-            parts.at[blockIdx.x] = b;
-        }
         if (vis > 0)
             wait(&sh.o, n - 1);
         fence_after();
@@ -680,16 +691,22 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                 if (n0 >= rows)
                     continue;
                 if (whole) {
-                    // lane pairs trade halves, so that each stores two columns of one row
+                    // lane pairs trade halves, so that each stores two columns of one row; all
+                    // is ready before the first store, behind which no shared load may move
+                    uint32_t two[8];
+                    uint16_t *to[8];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float e = vis > 0 ? o[k][i] * sh.f[n0 + i] : 0.0f, d = vis > 0 ? o[k][i + 1] * sh.f[n0 + i + 1] : 0.0f;
+                    for (int i = 0; i < 8; ++i) {
+                        const float e = vis > 0 ? o[k][2 * i] * sh.f[n0 + 2 * i] : 0.0f,
+                                    d = vis > 0 ? o[k][2 * i + 1] * sh.f[n0 + 2 * i + 1] : 0.0f;
                         const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? e : d, 1);
-                        const int row = n0 + i + (lane & 1);
-                        if (row < rows)
-                            *reinterpret_cast<uint32_t *>(a.out + sh.out[row] + d0 + (lane & ~1)) =
-                                lane & 1 ? pack_bf16(got, d) : pack_bf16(e, got);
+                        two[i] = lane & 1 ? pack_bf16(got, d) : pack_bf16(e, got);
+                        to[i] = a.out + sh.out[n0 + 2 * i + (lane & 1)] + d0 + (lane & ~1);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n0 + 2 * i + (lane & 1) < rows)
+                            *reinterpret_cast<uint32_t *>(to[i]) = two[i];
                 } else {
                     float *to = parts.o + (size_t(slot) * kMaxRows + n0) * W8_LATENT_DIM + d0 + lane;
 #pragma unroll
@@ -721,7 +738,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             bar_init(&sh.back_full[i], 1);
             bar_init(&sh.back_free[i], 1);
         }
-        bar_init(&sh.q, kSoftThreads);
+        bar_init(&sh.q, 32);
+        bar_init(&sh.q_free, 1);
         bar_init(&sh.s[0], 1);
         bar_init(&sh.s[1], 1);
         bar_init(&sh.s_free[0], kSoftThreads);
@@ -840,6 +858,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         return role == kCopyWarp    ? copy_role<NR>(a, map, w, sm, sh, rows_max <= NR)
                : role == kScoreWarp ? score_role<NR>(a, w, sm, sh, tm_s)
                : role == kOutWarp   ? out_role<NR>(a, w, sm, sh, tmem)
+               : role == kQueryWarp ? query_role<NR>(a, w, sm, sh, lane)
                                     : softmax_role<NR>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid);
     };
     const bool ok = nr == 64   ? roles(std::integral_constant<int, 64>{})
