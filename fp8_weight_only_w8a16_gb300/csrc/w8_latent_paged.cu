@@ -151,13 +151,15 @@ __device__ __forceinline__ int seen(const Request &q, int i)
     const int64_t n = int64_t(q.len) - q.q + i + 1;
     return int(n < 0 ? 0 : n > q.len ? q.len : n);
 }
-// Tiles of group g: those its last row sees, one (of nothing) if that is none.
-__device__ __forceinline__ int group_tiles(const Request &q, int heads, int nr, int g)
+// The query token of a row of the request; most requests have one.
+__device__ __forceinline__ int token_of(const Request &q, int heads, int row) { return q.q == 1 ? 0 : row / heads; }
+// Cached tokens that the last row of group g sees.
+__device__ __forceinline__ int group_sees(const Request &q, int heads, int nr, int g)
 {
-    const int last = min((g + 1) * nr, q.q * heads) - 1;
-    const int n = (seen(q, last / heads) + kTile - 1) / kTile;
-    return n < 1 ? 1 : n;
+    return seen(q, token_of(q, heads, min((g + 1) * nr, q.q * heads) - 1));
 }
+// Their tiles, one (of nothing) if there are none.
+__device__ __forceinline__ int tiles_of_sees(int vis) { return vis < 1 ? 1 : (vis + kTile - 1) / kTile; }
 __device__ __forceinline__ int groups_of(const Request &q, int heads, int nr) { return (q.q * heads + nr - 1) / nr; }
 
 // One CTA's place in the line, a run of one group at a time.  Every role walks
@@ -166,12 +168,12 @@ struct Walk {
     int64_t pos, end;  // the next tile's place, the CTA's last + 1
     int r, g, off;     // its request, group, place in the group
     Request req;
-    int tiles;         // of the group
+    int vis, tiles;    // what the group's last row sees
     int run;           // tiles of this run
 
     __device__ __forceinline__ bool next(const w8_latent_paged &a, int nr, bool first)
     {
-        if (!first) {
+        if (!first) { // the first request comes with the place
             pos += run + kBegin;
             off = 0;
             if (pos < end && ++g >= groups_of(req, a.n_heads, nr)) {
@@ -180,12 +182,11 @@ struct Walk {
                     req = request_of(a, ++r);
                 while (req.q == 0 && r + 1 < a.n_req);
             }
-        } else if (pos < end) {
-            req = request_of(a, r);
         }
         if (pos >= end)
             return false;
-        tiles = group_tiles(req, a.n_heads, nr, g);
+        vis = group_sees(req, a.n_heads, nr, g);
+        tiles = tiles_of_sees(vis);
         run = int(min(int64_t(tiles - off), end - pos));
         return true;
     }
@@ -199,6 +200,7 @@ struct Shared {
     int64_t sum[kPagedThreads / 32];
     int max[kPagedThreads / 32], few[kPagedThreads / 32];
     int start[4];
+    Request req;
     uint32_t tmem;
     float f[kMaxRows], top[2][kMaxRows];
 };
@@ -218,12 +220,6 @@ struct Turn {
     }
 };
 
-// Keys that the last row of the walk's group sees.
-__device__ __forceinline__ int group_sees(const w8_latent_paged &a, const Walk &w, int nr)
-{
-    return seen(w.req, (min((w.g + 1) * nr, w.req.q * a.n_heads) - 1) / a.n_heads);
-}
-
 // ---- copies ---------------------------------------------------------------
 // One lane does it all: two waits, two byte counts and 9 BOXES copies a tile.
 // (The loop must be short: with four half-size units a tile, votes and a
@@ -240,7 +236,7 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
     bool ok = true;
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
         const int32_t *table = a.block_table + int64_t(w.r) * a.ld_table;
-        const int vis = group_sees(a, w, NR);
+        const int vis = w.vis;
         const int end = vis > 0 ? w.off + w.run : w.off; // a group that sees nothing has a tile of nothing
         int pages[BOXES], ahead[BOXES]; // the next tile's pages are fetched ahead
         auto fetch = [&](int (&pg)[BOXES], int t) {
@@ -328,7 +324,7 @@ __device__ __forceinline__ bool score_role(const w8_latent_paged &a, Walk w, uin
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(bar, parity & 1)); };
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
-        if (group_sees(a, w, NR) == 0)
+        if (w.vis == 0)
             continue;
         wait(&sh.q, uint32_t(runs));
         ++runs;
@@ -388,7 +384,7 @@ __device__ __forceinline__ bool out_role(const w8_latent_paged &a, Walk w, uint8
     int n = 0;
     bool ok = true;
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
-        if (group_sees(a, w, NR) == 0)
+        if (w.vis == 0)
             continue;
         for (int t = 0; ok && t < w.run; ++t, ++n) {
             ok = __all_sync(0xffffffffu, bar_wait(&sh.p, uint32_t(n & 1)));
@@ -433,7 +429,7 @@ __device__ __forceinline__ bool query_role(const w8_latent_paged &a, Walk w, uin
     int runs = 0; // with keys
     bool ok = true;
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
-        if (group_sees(a, w, NR) == 0)
+        if (w.vis == 0)
             continue;
         // the last run's scores are made
         if (runs > 0)
@@ -442,7 +438,7 @@ __device__ __forceinline__ bool query_role(const w8_latent_paged &a, Walk w, uin
             break;
         ++runs;
         const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
-        int row = lane >> 3, tok = (row0 + row) / a.n_heads, head = row0 + row - tok * a.n_heads;
+        int row = lane >> 3, tok = token_of(w.req, a.n_heads, row0 + row), head = row0 + row - tok * a.n_heads;
 #pragma unroll 2
         for (; row < NR; row += 4) {
             const bool some = row < rows;
@@ -485,14 +481,14 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
     int n = 0; // tiles so far
     for (bool have = w.next(a, NR, true); have;) {
         const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
-        const int vis = seen(w.req, (row0 + rows - 1) / a.n_heads);
+        const int vis = w.vis;
         // how many keys this thread's rows see
         int lim[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            lim[h] = row_h[h] < rows ? seen(w.req, (row0 + row_h[h]) / a.n_heads) : 0;
+            lim[h] = row_h[h] < rows ? seen(w.req, token_of(w.req, a.n_heads, row0 + row_h[h])) : 0;
         if (tid < rows) {
-            const int tok = (row0 + tid) / a.n_heads, head = row0 + tid - tok * a.n_heads;
+            const int tok = token_of(w.req, a.n_heads, row0 + tid), head = row0 + tid - tok * a.n_heads;
             sh.out[tid] = (w.req.q0 + tok) * a.ld_out_tok + head * a.ld_out_head;
         }
         if (w.off > 0 && tid == 0) {
@@ -771,7 +767,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                 sum += int64_t(n) * max((q.len + kTile - 1) / kTile, 1);
             else
                 for (int g = 0; g < n; ++g)
-                    sum += group_tiles(q, a.n_heads, nr, g);
+                    sum += tiles_of_sees(group_sees(q, a.n_heads, nr, g));
         }
         return sum;
     };
@@ -829,13 +825,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             const Request q = r == r0 ? held : request_of(a, r);
             const int n = groups_of(q, a.n_heads, nr);
             for (int g = 0; g < n; ++g) {
-                const int t = kBegin + group_tiles(q, a.n_heads, nr, g);
+                const int t = kBegin + tiles_of_sees(group_sees(q, a.n_heads, nr, g));
                 if (at <= w.pos && w.pos < at + t) {
                     const int place = int(w.pos - at);
                     sh.start[0] = r;
                     sh.start[1] = g;
                     sh.start[2] = max(place - kBegin, 0);
                     sh.start[3] = max(kBegin - place, 0);
+                    sh.req = q;
                 }
                 at += t;
             }
@@ -849,6 +846,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         w.r = sh.start[0];
         w.g = sh.start[1];
         w.off = sh.start[2];
+        w.req = sh.req;
         w.pos += sh.start[3]; // past the group's begin; a CTA may have nothing else
     }
     const Parts parts = parts_of(ws, int(gridDim.x));
