@@ -28,29 +28,29 @@
 // in shared memory, and redone when some row has passed its reference), 8 copies
 // (tensor-map boxes of min(page, 64) tokens x 64 columns), 9 and 10 issue the two
 // products (a warp each, so that a tile's second product does not wait for the
-// next tile's copies), 11 loads the queries.  Two tiles are in flight, each in two halves: columns
-// 0 .. 255, freed when the second product has passed over them, and the rest.
-// The next group's queries are loaded and scored while this one's output is
-// stored.
+// next tile's copies), 11 loads the queries.  Two tiles are in flight, each in
+// two halves: columns 0 .. 255, freed when the second product has passed over
+// them, and the rest.  The next group's queries are loaded and scored while this
+// one's output is stored.
 // The reference moves only when a row's maximum passes it by 2^8 (p stays
 // below 2^8, and 2^8 of fp32's range costs no precision): O is then rescaled
 // in tensor memory, for most inputs once or twice in the first tiles.
 //
 // The work is cut by tiles, not by requests: all groups' tiles in one line,
-// an equal run a CTA, one CTA an SM.  A group's begin takes four places of the
-// line too, for its queries' load and its output's store cost a CTA about as
-// much as four tiles (24 requests of 1 to 4 query tokens, 64 heads: 80.3 us
-// with no such place, 75.4 with two, 72.7 with four, 75.6 with eight; 400
-// requests of up to 2000 tokens 140, 126, 118 with none, two, four); cuts that
+// an equal run a CTA, one CTA an SM.  A group's begin takes two places of the
+// line too, for the step from one group to the next costs a CTA about as much as
+// two tiles (with no, one, two and four such places, 64 heads: 24 requests of 1
+// to 4 query tokens 75.5, 73.0, 72.4, 73.4 us; 400 requests of up to 2000 tokens
+// 121.6, 116.0, 109.7, 110.1; 16 heads, two and four: 89.7, 91.7); cuts that
 // fall there move to the group's first tile, and split no group.  A group that
 // more than one run touches leaves its parts (O, m, z in fp32) in the
 // workspace, and a second kernel joins them.  Lengths are read on the device;
 // the line's length picks NR: 64 rows a group, or fewer when there are not
 // enough tiles to give every SM one.
 //
-// Measured (replayed, 64 heads): 128 requests of up to 16384 tokens 202 us,
-// 5.8 TB/s of HBM in the first kernel, about the rate of a copy; 24 requests of
-// 1 to 4 query tokens over up to 8111 tokens 73 us, bound by the chain copy -
+// Measured (replayed, 64 heads): 128 requests of up to 16384 tokens 200 us,
+// 5.9 TB/s of HBM in the first kernel, about the rate of a copy; 24 requests of
+// 1 to 4 query tokens over up to 8111 tokens 72 us, bound by the chain copy -
 // scores - softmax - output with two tiles in flight (2900 cycles a tile, the
 // tensor cores' share 1920) and by the parts (26 MB written and read back); one
 // request of 1531 tokens 13 us, latency.
@@ -82,7 +82,7 @@ constexpr int kPagedThreads = 384, kSoftThreads = 256, kCopyWarp = 8, kScoreWarp
 constexpr int kMaxSlots = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
-constexpr int kBegin = 4;                    // places of a group's begin in the line
+constexpr int kBegin = 2;                    // places of a group's begin in the line
 constexpr float kRaise = 8.0f;               // log2 of how far a row's weights may pass 1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
