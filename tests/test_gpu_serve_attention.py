@@ -114,6 +114,19 @@ def test_paged_many_requests(serve):
     Paged(lens, [1] * 700, 8, 16, seed=5).check(serve)
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 37, 75, 76, 77, 151, 152, 153, 305])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_paged_cuts_of_the_work(serve, n, heads):
+    """One-tile requests from fewer than there are SMs to more, with and without a long one among
+    them: cuts fall on a request's begin, beside it and inside it, and some SMs have no work."""
+    for long in (None, 0, n // 2, n - 1):
+        lens = [1 + (17 * i) % 64 for i in range(n)]
+        if long is not None:
+            lens[long] = 2500
+        q_lens = [1 + (i % 5 == 4) for i in range(n)]
+        Paged([max(a, b) for a, b in zip(lens, q_lens)], q_lens, heads, 16, seed=n).check(serve)
+
+
 @pytest.mark.parametrize("page", [16, 256, 1024])
 def test_paged_strides(serve, page):
     Paged([200, 77, 1030], [1, 2, 1], 20, page, seed=page, tok_pad=64, page_pad=8 * 13, q_pad=8).check(serve)
