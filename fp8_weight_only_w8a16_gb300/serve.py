@@ -128,6 +128,14 @@ def _cache_fields(cache: torch.Tensor) -> tuple:
     return cache.data_ptr(), page if n > 1 else max(page, size * tok), tok, n, size
 
 
+def _table(t: torch.Tensor, n: int) -> tuple[int, int, int]:
+    """Pointer, row stride and width of a page table of at least n rows.  The
+    stride goes out as it is: rows that share their storage (expand) are the
+    library's to refuse."""
+    assert t.dim() == 2 and t.stride(1) == 1 and t.dtype == torch.int32 and t.shape[0] >= n
+    return t.data_ptr(), t.stride(0) if n > 1 else t.shape[1], t.shape[1]
+
+
 def _workspace(ws: torch.Tensor | None) -> tuple:
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
@@ -145,12 +153,9 @@ def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_size: int,
     write the tables, lengths, offsets, slots and positions of the step (one
     kernel launch).  ``status`` is 0 when everything fitted."""
     n, toks = ctx_lens.numel(), slots.numel()
-    assert block_table.dim() == 2 and block_table.stride(1) == 1 and block_table.dtype == torch.int32
-    assert block_table.shape[0] >= n
-    width = block_table.shape[1]
     _check(lib.w8_block_tables(
         _ints(ctx_lens), _ints(new_lens, n=n), n, page_size, _ints(free_pages), free_pages.numel(),
-        _ints(free_head, n=1), block_table.data_ptr(), max(block_table.stride(0), width), width,
+        _ints(free_head, n=1), *_table(block_table, n),
         _ints(seq_lens, n=n), _ints(cu_new, n=n + 1), _ints(slots, torch.int64),
         _ints(positions, n=toks), toks, _ints(free_head_out, n=1), _ints(status, n=1),
         _stream(stream)))
@@ -190,12 +195,10 @@ def latent_attn_paged(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: torch.Te
     [pages, page_size, 576], out [T, H, 512] (two kernel launches)."""
     toks, heads = q_lat.shape[0], q_lat.shape[1]
     n = seq_lens.numel()
-    assert block_table.dim() == 2 and block_table.stride(1) == 1 and block_table.dtype == torch.int32
-    assert block_table.shape[0] >= n
-    width = block_table.shape[1]
+    table, ld_table, width = _table(block_table, n)
     args = _PAGED.pack(
         *_heads(q_lat, toks, heads, LATENT_DIM), *_heads(q_rope, toks, heads, LATENT_ROPE),
-        *_cache_fields(cache), block_table.data_ptr(), max(block_table.stride(0), width),
+        *_cache_fields(cache), table, ld_table,
         _ints(seq_lens), _ints(cu_q, n=n + 1), *_heads(out, toks, heads, LATENT_DIM),
         _ints(lse, torch.float32, toks * heads) if lse is not None else 0,
         width, n, toks, heads, scale)
