@@ -6,7 +6,8 @@ What a serving step runs between and after the projections: ``block_tables``
 ``latent_attn_paged`` (absorbed form over the paged cache),
 ``latent_attn_expanded`` (expanded form over a prompt) and ``token_logprobs``.
 Every call takes its outputs and its workspace from the caller and is
-asynchronous on ``stream`` (default: the current stream).
+asynchronous on ``stream`` (default: the current stream).  All tensors are on
+the GPU.
 """
 from __future__ import annotations
 
@@ -100,20 +101,20 @@ def _stream(stream) -> int:
 
 
 def _ints(t: torch.Tensor, dtype: torch.dtype = torch.int32, n: int | None = None) -> int:
-    assert t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() >= n)
+    assert t.is_cuda and t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() >= n)
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, cols: int) -> tuple[int, int]:
     """Pointer and row stride of a 2-D bf16 operand."""
     row, one = t.stride()
-    assert t.shape[1] == cols and one == 1 and t.element_size() == 2
+    assert t.is_cuda and t.shape[1] == cols and one == 1 and t.element_size() == 2
     return t.data_ptr(), row
 
 
 def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int, int]:
     """Pointer, token stride and head stride of a bf16 operand [toks, heads, cols]."""
-    assert t.shape == (toks, heads, cols) and t.element_size() == 2
+    assert t.is_cuda and t.shape == (toks, heads, cols) and t.element_size() == 2
     tok, head, one = t.stride()
     assert one == 1
     # the stride of an axis of one entry says nothing: give one that fits
@@ -123,7 +124,7 @@ def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int,
 def _cache_fields(cache: torch.Tensor) -> tuple:
     page, tok, one = cache.stride()
     n, size, cols = cache.shape
-    assert cols == LATENT_ROW and one == 1 and cache.element_size() == 2
+    assert cache.is_cuda and cols == LATENT_ROW and one == 1 and cache.element_size() == 2
     tok = tok if size > 1 else max(tok, LATENT_ROW)
     return cache.data_ptr(), page if n > 1 else max(page, size * tok), tok, n, size
 
@@ -132,11 +133,12 @@ def _table(t: torch.Tensor, n: int) -> tuple[int, int, int]:
     """Pointer, row stride and width of a page table of at least n rows.  The
     stride goes out as it is: rows that share their storage (expand) are the
     library's to refuse."""
-    assert t.dim() == 2 and t.stride(1) == 1 and t.dtype == torch.int32 and t.shape[0] >= n
+    assert t.is_cuda and t.dim() == 2 and t.stride(1) == 1 and t.dtype == torch.int32 and t.shape[0] >= n
     return t.data_ptr(), t.stride(0) if n > 1 else t.shape[1], t.shape[1]
 
 
 def _workspace(ws: torch.Tensor | None) -> tuple:
+    assert ws is None or ws.is_cuda
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
@@ -244,7 +246,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprob: torch.Te
     """The log probability of tokens[i] under logits[i] (bf16 or fp32), the
     row's entropy and its top_ids.shape[1] most likely tokens (one kernel
     launch)."""
-    assert logits.dim() == 2 and logits.stride(1) == 1
+    assert logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1
     rows, vocab = logits.shape
     dtype = {torch.bfloat16: LOGITS_BF16, torch.float32: LOGITS_F32}.get(logits.dtype, 0)
     top = 0 if top_ids is None else top_ids.shape[1]

@@ -72,3 +72,41 @@ def test_table_stride_is_the_tensors_own(calls, call, table, n, want):
     """The table's row stride goes to the library as it is (which refuses one below the width), except
     where there is one row."""
     assert strides(calls, call, table, n) == want
+
+
+# every call with small operands, by name
+OPERANDS = {
+    "block_tables": lambda: dict(
+        ctx_lens=i32(3), new_lens=i32(3), page_size=16, free_pages=i32(9), free_head=i32(1), block_table=i32(3, 4),
+        seq_lens=i32(3), cu_new=i32(4), slots=on_gpu(torch.zeros(5, dtype=torch.int64)), positions=i32(5),
+        free_head_out=i32(1), status=i32(1)),
+    "latent_cache_write": lambda: dict(
+        latent=bf16(5, 512), rope=bf16(5, 64), slots=on_gpu(torch.zeros(5, dtype=torch.int64)), cache=bf16(4, 16, 576)),
+    "latent_attn_paged": lambda: dict(
+        q_lat=bf16(3, 2, 512), q_rope=bf16(3, 2, 64), cache=bf16(4, 16, 576), block_table=i32(3, 4), seq_lens=i32(3),
+        cu_q=i32(4), scale=0.1, out=bf16(3, 2, 512), lse=on_gpu(torch.zeros(3, 2)),
+        workspace=on_gpu(torch.zeros(256, dtype=torch.uint8))),
+    "latent_attn_expanded": lambda: dict(
+        q_nope=bf16(3, 2, 128), q_rope=bf16(3, 2, 64), k_nope=bf16(5, 2, 128), k_rope=bf16(5, 64), v=bf16(5, 2, 128),
+        cu_q=i32(3), cu_k=i32(3), scale=0.1, causal=True, out=bf16(3, 2, 128), lse=on_gpu(torch.zeros(3, 2))),
+    "token_logprobs": lambda: dict(
+        logits=bf16(2, 100), tokens=i32(2), logprob=on_gpu(torch.zeros(2)), entropy=on_gpu(torch.zeros(2)), top_ids=i32(2, 3),
+        top_logprobs=on_gpu(torch.zeros(2, 3)), workspace=on_gpu(torch.zeros(256, dtype=torch.uint8))),
+}
+TENSORS = [(f, k) for f, make in OPERANDS.items() for k, v in make().items() if isinstance(v, torch.Tensor)]
+
+
+@pytest.mark.parametrize("name", OPERANDS)
+def test_operands_reach_the_library(calls, name):
+    getattr(serve, name)(**OPERANDS[name]())
+    assert [c[0] for c in calls] == ["w8_" + name]
+
+
+@pytest.mark.parametrize("name,operand", TENSORS)
+def test_host_tensors_are_refused(calls, name, operand):
+    """A tensor on the host is no device pointer: the library is not called."""
+    args = OPERANDS[name]()
+    args[operand] = args[operand].as_subclass(torch.Tensor)
+    with pytest.raises(AssertionError):
+        getattr(serve, name)(**args)
+    assert not calls
