@@ -108,13 +108,13 @@ def _ints(t: torch.Tensor, dtype: torch.dtype = torch.int32, n: int | None = Non
 def _rows(t: torch.Tensor, cols: int) -> tuple[int, int]:
     """Pointer and row stride of a 2-D bf16 operand."""
     row, one = t.stride()
-    assert t.is_cuda and t.shape[1] == cols and one == 1 and t.element_size() == 2
+    assert t.is_cuda and t.shape[1] == cols and one == 1 and t.dtype == torch.bfloat16
     return t.data_ptr(), row
 
 
 def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int, int]:
     """Pointer, token stride and head stride of a bf16 operand [toks, heads, cols]."""
-    assert t.is_cuda and t.shape == (toks, heads, cols) and t.element_size() == 2
+    assert t.is_cuda and t.shape == (toks, heads, cols) and t.dtype == torch.bfloat16
     tok, head, one = t.stride()
     assert one == 1
     # the stride of an axis of one entry says nothing: give one that fits
@@ -124,7 +124,7 @@ def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int,
 def _cache_fields(cache: torch.Tensor) -> tuple:
     page, tok, one = cache.stride()
     n, size, cols = cache.shape
-    assert cache.is_cuda and cols == LATENT_ROW and one == 1 and cache.element_size() == 2
+    assert cache.is_cuda and cols == LATENT_ROW and one == 1 and cache.dtype == torch.bfloat16
     tok = tok if size > 1 else max(tok, LATENT_ROW)
     return cache.data_ptr(), page if n > 1 else max(page, size * tok), tok, n, size
 

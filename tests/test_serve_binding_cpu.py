@@ -110,3 +110,23 @@ def test_host_tensors_are_refused(calls, name, operand):
     with pytest.raises(AssertionError):
         getattr(serve, name)(**args)
     assert not calls
+
+
+@pytest.mark.parametrize("name,operand", [(f, k) for f, k in TENSORS if k != "logits" and OPERANDS[f]()[k].dtype == torch.bfloat16])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int16, torch.float32])
+def test_other_types_than_bf16_are_refused(calls, name, operand, dtype):
+    """16 bits of another type would be read as bf16."""
+    args = OPERANDS[name]()
+    args[operand] = on_gpu(torch.zeros(args[operand].shape, dtype=dtype))
+    with pytest.raises(AssertionError):
+        getattr(serve, name)(**args)
+    assert not calls
+
+
+def test_logits_of_another_type_are_refused(monkeypatch):
+    """The library tells the logits' type by a code; fp16 has none."""
+    monkeypatch.setattr(serve, "_stream", lambda stream: None)
+    args = OPERANDS["token_logprobs"]()
+    args["logits"] = on_gpu(torch.zeros(2, 100, dtype=torch.float16))
+    with pytest.raises(serve.W8Error):
+        serve.token_logprobs(**args)
