@@ -142,8 +142,15 @@ def _workspace(ws: torch.Tensor | None) -> tuple:
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
-def _sms(device) -> int:
-    return torch.cuda.get_device_properties(device or torch.cuda.current_device()).multi_processor_count
+def _device(device) -> torch.device:
+    """The GPU of a workspace: a device, its name or its number; None: the current one."""
+    if device is None:
+        device = torch.cuda.current_device()
+    return torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+
+
+def _sms(device: torch.device) -> int:
+    return torch.cuda.get_device_properties(device).multi_processor_count
 
 
 def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_size: int,
@@ -184,8 +191,9 @@ def latent_paged_workspace_bytes(n_tok: int, n_heads: int, n_req: int, sm_count:
 
 def new_latent_paged_workspace(n_tok: int, n_heads: int, n_req: int, device=None) -> torch.Tensor:
     """A workspace for latent_attn_paged calls of up to these counts."""
+    device = _device(device)
     nbytes = latent_paged_workspace_bytes(n_tok, n_heads, n_req, _sms(device))
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def latent_attn_paged(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: torch.Tensor,
@@ -235,8 +243,9 @@ def logprobs_workspace_bytes(n_rows: int, vocab: int, top: int, sm_count: int) -
 def new_logprobs_workspace(n_rows: int, vocab: int, top: int = 0, device=None) -> torch.Tensor:
     """A zero-filled workspace for token_logprobs calls of this shape (its
     counters must start at zero)."""
+    device = _device(device)
     nbytes = logprobs_workspace_bytes(n_rows, vocab, top, _sms(device))
-    return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprob: torch.Tensor,

@@ -130,3 +130,29 @@ def test_logits_of_another_type_are_refused(monkeypatch):
     args["logits"] = on_gpu(torch.zeros(2, 100, dtype=torch.float16))
     with pytest.raises(serve.W8Error):
         serve.token_logprobs(**args)
+
+
+@pytest.mark.parametrize("device,want", [
+    (0, "cuda:0"), (1, "cuda:1"), (2, "cuda:2"), (None, "cuda:1"), ("cuda:0", "cuda:0"), (torch.device("cuda", 0), "cuda:0")])
+def test_workspaces_are_made_for_the_device_that_is_named(monkeypatch, device, want):
+    """... and sized for its SMs, device 0 too, with device 1 the current one."""
+    made = []
+    sms = {0: 10, 1: 152, 2: 80}
+
+    class Properties:
+        def __init__(self, device):
+            self.multi_processor_count = sms[torch.device(device).index if not isinstance(device, int) else device]
+
+    def make(n, dtype, device):
+        made.append((n, str(device)))
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "get_device_properties", Properties)
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(torch, "zeros", make)
+    serve.new_latent_paged_workspace(4, 64, 2, device=device)
+    serve.new_logprobs_workspace(2, 154880, 5, device=device)
+    n = sms[torch.device(want).index]
+    assert [d for _, d in made] == [want] * 2
+    assert made[0][0] == serve.latent_paged_workspace_bytes(4, 64, 2, n)
+    assert made[1][0] >= serve.logprobs_workspace_bytes(2, 154880, 5, n)
