@@ -109,7 +109,7 @@ def _rows(t: torch.Tensor, cols: int) -> tuple[int, int]:
     """Pointer and row stride of a 2-D bf16 operand."""
     row, one = t.stride()
     assert t.is_cuda and t.shape[1] == cols and one == 1 and t.dtype == torch.bfloat16
-    return t.data_ptr(), row
+    return t.data_ptr(), row if t.shape[0] > 1 else cols
 
 
 def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int, int]:
@@ -118,15 +118,16 @@ def _heads(t: torch.Tensor, toks: int, heads: int, cols: int) -> tuple[int, int,
     tok, head, one = t.stride()
     assert one == 1
     # the stride of an axis of one entry says nothing: give one that fits
-    return t.data_ptr(), tok if toks > 1 else max(tok, -(-cols // 8) * 8), head if heads > 1 else max(head, cols)
+    head = head if heads > 1 else cols
+    return t.data_ptr(), tok if toks > 1 else heads * head, head
 
 
 def _cache_fields(cache: torch.Tensor) -> tuple:
     page, tok, one = cache.stride()
     n, size, cols = cache.shape
     assert cache.is_cuda and cols == LATENT_ROW and one == 1 and cache.dtype == torch.bfloat16
-    tok = tok if size > 1 else max(tok, LATENT_ROW)
-    return cache.data_ptr(), page if n > 1 else max(page, size * tok), tok, n, size
+    tok = tok if size > 1 else LATENT_ROW
+    return cache.data_ptr(), page if n > 1 else size * tok, tok, n, size
 
 
 def _table(t: torch.Tensor, n: int) -> tuple[int, int, int]:

@@ -156,3 +156,30 @@ def test_workspaces_are_made_for_the_device_that_is_named(monkeypatch, device, w
     assert [d for _, d in made] == [want] * 2
     assert made[0][0] == serve.latent_paged_workspace_bytes(4, 64, 2, n)
     assert made[1][0] >= serve.logprobs_workspace_bytes(2, 154880, 5, n)
+
+
+def test_the_stride_of_one_entry_says_nothing(calls):
+    """One token, one head, one page, a page of one token: a stride that is no multiple of 8, or none at
+    all, comes with a slice or an expand of such an axis and refuses nothing."""
+    def one(*shape):  # its first axis an odd number of elements apart, and one entry long
+        n = 1
+        for x in shape[1:]:
+            n *= x
+        return on_gpu(torch.zeros(2 * n + 13, dtype=torch.bfloat16).as_strided(shape, (n + 13,) + torch.empty(shape).stride()[1:]))
+
+    serve.latent_attn_paged(one(1, 3, 512), one(1, 3, 64), one(1, 16, 576), i32(1, 4), i32(1), i32(2), 0.1, one(1, 3, 512))
+    serve.latent_attn_paged(one(1, 3, 512).transpose(0, 1), one(1, 3, 64).transpose(0, 1), one(1, 4, 576).transpose(0, 1),
+                            i32(1, 4), i32(1), i32(2), 0.1, one(1, 3, 512).transpose(0, 1))
+    serve.latent_attn_expanded(one(1, 3, 128), one(1, 3, 64), one(1, 3, 128), one(1, 64), one(1, 3, 128), i32(2), i32(2),
+                               0.1, True, one(1, 3, 128))
+    serve.latent_cache_write(one(1, 512), one(1, 64), on_gpu(torch.zeros(1, dtype=torch.int64)), one(1, 16, 576))
+    serve.latent_attn_paged(bf16(1, 512).expand(1, 1, 512), bf16(64).expand(1, 1, 64), bf16(16, 576).expand(1, 16, 576),
+                            i32(1, 4), i32(1), i32(2), 0.1, bf16(1, 1, 512))
+    a, b, c, d, e = (args for _, args in calls)
+    pack = serve._PAGED.unpack
+    assert pack(a[0])[1:3] == (1536, 512) and pack(a[0])[4:6] == (192, 64) and pack(a[0])[7:9] == (16 * 576, 576)
+    assert pack(b[0])[1:3] == (512, 512) and pack(b[0])[4:6] == (64, 64) and pack(b[0])[7:9] == (576, 576)
+    fields = serve._EXPANDED.unpack(c[0])
+    assert fields[1:3] == (384, 128) and fields[4:6] == (192, 64) and fields[7:9] == (384, 128) and fields[10] == 64
+    assert d[1] == 512 and d[3] == 64
+    assert pack(e[0])[1:3] == (512, 512) and pack(e[0])[7:9] == (16 * 576, 576)
