@@ -62,6 +62,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "w8_copies.h"
 #include "w8_device.cuh"
 #include "w8_serve_internal.h"
 #include "w8_tcgen.cuh"
@@ -231,8 +232,8 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
     constexpr int kBox = kTile / BOXES;
     const int page = a.cache.page_size, shift = 31 - __clz(page);
     const uint32_t front = smem_addr(sm + lay.front), back = smem_addr(sm + lay.back);
-    Turn f, b;
-    int tiles = 0; // copied so far
+    Ring<lay.fronts> f;
+    Ring<lay.backs> b;
     bool ok = true;
     for (bool first = true; ok && w.next(a, NR, first); first = false) {
         const int32_t *table = a.block_table + int64_t(w.r) * a.ld_table;
@@ -247,7 +248,7 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
             }
         };
         fetch(pages, w.off);
-        for (int t = w.off; t < end; ++t, ++tiles) {
+        for (int t = w.off; t < end; ++t) {
             fetch(ahead, t + 1);
             const int left = min(vis - t * kTile, kTile);
             const int need = (left + kBox - 1) / kBox;            // boxes with a key that is seen
@@ -255,8 +256,7 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
 #pragma unroll
             for (int i = 0; i < BOXES; ++i) // a number that is no page reads as zeros
                 pages[i] = pages[i] < 0 || pages[i] > a.cache.n_pages ? a.cache.n_pages : pages[i];
-            if (tiles >= lay.fronts)
-                ok = bar_wait(&sh.front_free[f.k], f.parity ^ 1);
+            ok = f.take([&](int k, uint32_t parity) { return bar_wait(&sh.front_free[k], parity); });
             if (!ok)
                 break;
             bar_expect(&sh.front_full[f.k], uint32_t(kFront * kBox * 128) * need);
@@ -267,9 +267,8 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
                     if (i < need)
                         copy_box(front + uint32_t(f.k * kFront * kChunk + c * kChunk + i * kBox * 128), &map, 64 * c, y, pages[i],
                                  &sh.front_full[f.k], policy);
-            f.step(lay.fronts);
-            if (tiles >= lay.backs)
-                ok = bar_wait(&sh.back_free[b.k], b.parity ^ 1);
+            f.filled();
+            ok = b.take([&](int k, uint32_t parity) { return bar_wait(&sh.back_free[k], parity); });
             if (!ok)
                 break;
             bar_expect(&sh.back_full[b.k], uint32_t(kBack * kBox * 128) * need);
@@ -280,19 +279,15 @@ __device__ __forceinline__ bool copy_loop(const w8_latent_paged &a, const CUtens
                     if (i < need)
                         copy_box(back + uint32_t(b.k * kBack * kChunk + c * kChunk + i * kBox * 128), &map, 64 * (kFront + c), y,
                                  pages[i], &sh.back_full[b.k], policy);
-            b.step(lay.backs);
+            b.filled();
 #pragma unroll
             for (int i = 0; i < BOXES; ++i)
                 pages[i] = ahead[i];
         }
     }
     // the copies still in flight (there are any only after a wait elsewhere gave up)
-    if (!ok)
-        ++tiles; // a front half may be on its way without its back half
-    for (int i = max(0, tiles - lay.fronts); i < tiles; ++i)
-        bar_wait(&sh.front_full[i % lay.fronts], uint32_t((i / lay.fronts) & 1));
-    for (int i = max(0, tiles - lay.backs); i < tiles; ++i)
-        bar_wait(&sh.back_full[i % lay.backs], uint32_t((i / lay.backs) & 1));
+    f.drain([&](int k, uint32_t parity) { bar_wait(&sh.front_full[k], parity); });
+    b.drain([&](int k, uint32_t parity) { bar_wait(&sh.back_full[k], parity); });
     return ok;
 }
 template <int NR>
