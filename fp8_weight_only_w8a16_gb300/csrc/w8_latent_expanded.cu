@@ -23,6 +23,7 @@
 // / 128 in 11.8 us, bound by the chain scores - softmax - output of a tile; a
 // full tile of 192 + 64 / 256 takes 2566 cycles, 2048 of them steps, and wants
 // 50 bytes a cycle and SM from L2.
+#include "w8_copies.h"
 #include "w8_expanded.cuh"
 
 namespace w8 {
@@ -158,19 +159,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             for (int c = 0; c < S::kChunks; ++c)
                 copy_box(q + c * kRows * 128, c < DN / 64 ? &maps.q_nope : &maps.q_rope, c < DN / 64 ? 64 * c : 0, head, it.q0,
                          &sh.q, policy_normal());
-            int k = 0, used = 0;
-            uint32_t parity = 0;
+            Ring<S::kSlots> to;
             auto slot = [&]() { // the next slot, its old content read
-                if (used >= S::kSlots)
-                    ok = ok && bar_wait(&sh.free_[k], parity ^ 1);
-                ++used;
+                ok = ok && to.take([&](int k, uint32_t parity) { return bar_wait(&sh.free_[k], parity); });
                 return ok;
-            };
-            auto step = [&] {
-                if (++k == S::kSlots) {
-                    k = 0;
-                    parity ^= 1;
-                }
             };
             for (int i = 0; i <= it.tiles && ok; ++i) {
                 if (i < it.tiles) {
@@ -178,17 +170,17 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                     for (int g = 0; g < S::kKSlots; ++g) {
                         if (!slot())
                             break;
-                        bar_expect(&sh.full[k], S::kSlot);
+                        bar_expect(&sh.full[to.k], S::kSlot);
 #pragma unroll
                         for (int c = 0; c < S::kKChunks; ++c) {
                             const int chunk = g * S::kKChunks + c;
-                            const uint32_t dst = ring + uint32_t(k * S::kSlot + c * kKeys * 128);
+                            const uint32_t dst = ring + uint32_t(to.k * S::kSlot + c * kKeys * 128);
                             if (chunk < DN / 64)
-                                copy_box(dst, &maps.k_nope, 64 * chunk, head, it.k0 + i * kKeys, &sh.full[k], policy_normal());
+                                copy_box(dst, &maps.k_nope, 64 * chunk, head, it.k0 + i * kKeys, &sh.full[to.k], policy_normal());
                             else
-                                copy_box(dst, &maps.k_rope, 0, it.k0 + i * kKeys, &sh.full[k]);
+                                copy_box(dst, &maps.k_rope, 0, it.k0 + i * kKeys, &sh.full[to.k]);
                         }
-                        step();
+                        to.filled();
                     }
                 }
                 if (i > 0) {
@@ -196,22 +188,19 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                     for (int g = 0; g < S::kVSlots; ++g) {
                         if (!slot())
                             break;
-                        bar_expect(&sh.full[k], S::kSlot);
+                        bar_expect(&sh.full[to.k], S::kSlot);
 #pragma unroll
                         for (int c = 0; c < DV / 64; ++c)
-                            copy_box(ring + uint32_t(k * S::kSlot + c * 64 * 128), &maps.v, 64 * c, head,
-                                     it.k0 + (i - 1) * kKeys + 64 * g, &sh.full[k], policy_normal());
-                        step();
+                            copy_box(ring + uint32_t(to.k * S::kSlot + c * 64 * 128), &maps.v, 64 * c, head,
+                                     it.k0 + (i - 1) * kKeys + 64 * g, &sh.full[to.k], policy_normal());
+                        to.filled();
                     }
                 }
             }
-            // the copies still in flight (there are any only after a wait elsewhere gave up)
-            if (!ok) {
-                bar_wait(&sh.q, 0);
-                --used; // the slot that was not to be had
-                for (int i = max(0, used - S::kSlots); i < used; ++i)
-                    bar_wait(&sh.full[i % S::kSlots], uint32_t((i / S::kSlots) & 1));
-            }
+            // The copies still in flight.  (Not only where a wait of this lane gave up:
+            // the lanes that use them may have.)
+            bar_wait(&sh.q, 0);
+            to.drain([&](int k, uint32_t parity) { bar_wait(&sh.full[k], parity); });
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {

@@ -78,7 +78,7 @@ def test_ring_is_drained_wherever_its_reader_stops(tmp_path):
     run(tmp_path, RING)
 
 
-@pytest.mark.parametrize("kernel,rings", [("w8_latent_paged.cu", 2)])
+@pytest.mark.parametrize("kernel,rings", [("w8_latent_paged.cu", 2), ("w8_latent_expanded.cu", 1)])
 def test_kernels_drain_their_rings(kernel, rings):
     """Every ring of a copying lane is drained, whether or not the lane itself gave up."""
     text = open(os.path.join(CSRC, kernel)).read()
