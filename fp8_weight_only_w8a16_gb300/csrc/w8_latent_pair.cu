@@ -33,6 +33,9 @@
 // weights lie in the same columns, and nothing else is left to run meanwhile.
 // The rest is the 3400 cycles of an item's output, of which the next one's
 // scores hide about half, and the clock (the chip is at its power limit).
+#include <stddef.h>
+
+#include "w8_copies.h"
 #include "w8_expanded.cuh"
 
 namespace w8 {
@@ -72,6 +75,8 @@ struct Shared {
     int before[kExpThreads];     // query tiles up to each thread's run of requests, inclusive
     int count[kExpThreads / 32];
     uint32_t tmem;
+    int failed;                  // a wait of either CTA gave up
+    PairIssued issued[2];        // by this CTA, by the other
 };
 static_assert(sizeof(Shared) <= 2048, "shared memory");
 
@@ -84,12 +89,17 @@ struct Item {
     int head;
 };
 
-// The same place in the pair's first CTA.
-__device__ __forceinline__ uint32_t in_first(const void *p)
+// The same place in a CTA of the pair, in its first.
+__device__ __forceinline__ uint32_t in_cta(const void *p, int rank)
 {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
+}
+__device__ __forceinline__ uint32_t in_first(const void *p) { return in_cta(p, 0); }
+__device__ __forceinline__ void pair_store(uint32_t to, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
 }
 // Arrive at a barrier of either CTA.  What passes between the two CTAs this way
 // lies in tensor memory and in the async proxy's view of shared memory, completed
@@ -163,6 +173,25 @@ __device__ __forceinline__ int answered(const uint4 *answer)
                  : "memory");
     return some ? int(x >> 1) : -1;
 }
+
+// The barriers of a CTA, as pair_drain sees them.
+template <typename S>
+struct DrainBars {
+    Shared &sh;
+    __device__ __forceinline__ void forgo(uint64_t *bar, uint32_t bytes)
+    {
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+    }
+    __device__ __forceinline__ void wait_last(int s, uint32_t parity) { bar_wait(&sh.v_last[s], parity); }
+    __device__ __forceinline__ void wait_full(int s, uint32_t parity) { bar_wait(&sh.full[s], parity); }
+    __device__ __forceinline__ void expect_full(int s, bool values) { bar_expect(&sh.full[s], values ? S::kV : S::kK); }
+    __device__ __forceinline__ void forgo_full(int s, bool values) { forgo(&sh.full[s], values ? S::kV : S::kK); }
+    __device__ __forceinline__ void wait_queries(uint32_t parity) { bar_wait(&sh.q, parity); }
+    __device__ __forceinline__ void expect_queries() { bar_expect(&sh.q, S::kQ); }
+    __device__ __forceinline__ void forgo_queries() { forgo(&sh.q, S::kQ); }
+    __device__ __forceinline__ void wait_answer(int k, uint32_t parity) { bar_wait(&sh.next_full[k], parity); }
+    __device__ __forceinline__ void expect_answer(int k) { bar_expect(&sh.next_full[k], 16); }
+};
 
 __device__ __forceinline__ int queries(const w8_latent_expanded &a, int r, int &q0)
 {
@@ -247,6 +276,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         bar_init(&sh.done, 2 * kSoftWarps);
         bar_init(&sh.end, 1);
         bar_init_fence();
+        sh.failed = 0;
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
@@ -298,8 +328,9 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     };
 
     if (warp == kCopyWarp) {
-        int k = 0, used = 0, work = 0; // slot, slots used so far, items with keys
-        uint32_t parity = 0;
+        Ring<S::kSlots> to;
+        PairIssued did{};
+        int work = 0; // items with keys
         const uint32_t ring = smem_addr(s_ring), q = smem_addr(sm), q_bar = in_first(&sh.q);
         while (id >= 0) {
             // the answer for the item after this one
@@ -311,22 +342,16 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 if (rank == 0 && ok)
                     ask_next(&sh.next[n], &sh.next_full[n]);
             }
+            ++did.expects;
+            did.asks += rank == 0 && ok;
             __syncwarp();
             const Item it = find(a, sh, id, tiles_max, rank, lane);
             if (it.tiles > 0) {
                 uint32_t who;
                 if (elect_one(who)) {
                     auto slot = [&]() { // the next slot, its old content read
-                        if (used >= S::kSlots)
-                            ok = ok && bar_wait(&sh.free_[k], parity ^ 1);
-                        used += ok;
+                        ok = ok && to.take([&](int k, uint32_t parity) { return bar_wait(&sh.free_[k], parity); });
                         return ok;
-                    };
-                    auto step = [&] {
-                        if (++k == S::kSlots) {
-                            k = 0;
-                            parity ^= 1;
-                        }
                     };
                     if (work > 0)
                         ok = ok && bar_wait(&sh.q_free, uint32_t((work - 1) & 1));
@@ -338,14 +363,15 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                         for (int c = 0; c < S::kChunks; ++c)
                             pair_copy(q + c * kRows * 128, c < DN / 64 ? &maps.q_nope : &maps.q_rope, c < DN / 64 ? 64 * c : 0,
                                       it.head, it.q0, q_bar);
+                        ++did.queries;
                     }
                     for (int i = 0; i <= it.tiles; ++i) {
                         if (i < it.tiles) {
                             if (!slot())
                                 break;
-                            const uint32_t bar = in_first(&sh.full[k]), dst = ring + uint32_t(k * S::kSlot);
+                            const uint32_t bar = in_first(&sh.full[to.k]), dst = ring + uint32_t(to.k * S::kSlot);
                             if (rank == 0)
-                                bar_expect(&sh.full[k], 2 * S::kK);
+                                bar_expect(&sh.full[to.k], 2 * S::kK);
                             const int row = it.k0 + i * kKeys + rank * (kKeys / 2);
 #pragma unroll
                             for (int c = 0; c < S::kChunks; ++c) {
@@ -354,40 +380,60 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                                 else
                                     pair_copy(dst + c * S::kHalf, &maps.k_rope, 0, row, bar);
                             }
-                            step();
+                            did.full ^= 1u << to.k;
+                            did.values &= ~(1u << to.k);
+                            to.filled();
                         }
                         if (i > 0) {
                             if (!slot())
                                 break;
                             // the last tile's values count here: their rows past the keys are made zero before they are used
                             const bool last = i == it.tiles;
-                            const uint32_t bar = last ? smem_addr(&sh.v_last[k]) : in_first(&sh.full[k]);
+                            const uint32_t bar = last ? smem_addr(&sh.v_last[to.k]) : in_first(&sh.full[to.k]);
                             if (last)
-                                bar_expect(&sh.v_last[k], S::kV);
+                                bar_expect(&sh.v_last[to.k], S::kV);
                             else if (rank == 0)
-                                bar_expect(&sh.full[k], 2 * S::kV);
+                                bar_expect(&sh.full[to.k], 2 * S::kV);
 #pragma unroll
                             for (int c = 0; c < S::kRuns; ++c)
-                                pair_copy(ring + uint32_t(k * S::kSlot + c * S::kRun), &maps.v, rank * (DV / 2) + 64 * c, it.head,
+                                pair_copy(ring + uint32_t(to.k * S::kSlot + c * S::kRun), &maps.v, rank * (DV / 2) + 64 * c, it.head,
                                           it.k0 + (i - 1) * kKeys, bar);
-                            step();
+                            if (last) {
+                                did.last ^= 1u << to.k;
+                            } else {
+                                did.full ^= 1u << to.k;
+                                did.values |= 1u << to.k;
+                            }
+                            to.filled();
                         }
                     }
                 }
                 __syncwarp();
                 ok = __shfl_sync(0xffffffffu, ok, who);
-                k = __shfl_sync(0xffffffffu, k, who);
-                used = __shfl_sync(0xffffffffu, used, who);
-                parity = __shfl_sync(0xffffffffu, parity, who);
+                to.k = __shfl_sync(0xffffffffu, to.k, who);
+                to.used = __shfl_sync(0xffffffffu, to.used, who);
+                to.parity = __shfl_sync(0xffffffffu, to.parity, who);
+                did.full = __shfl_sync(0xffffffffu, did.full, who);
+                did.values = __shfl_sync(0xffffffffu, did.values, who);
+                did.last = __shfl_sync(0xffffffffu, did.last, who);
+                did.queries = __shfl_sync(0xffffffffu, did.queries, who);
                 ++work;
             }
             next();
         }
-        // After a wait that gave up, copies may still be on their way into this
-        // CTA, counted on barriers that nobody reads any more: give them time.
-        if (!ok)
-            for (int i = 0; i < 1000; ++i)
-                __nanosleep(1000);
+        // what has been issued, for either CTA's last waits
+        did.used = uint32_t(to.used);
+        if (lane == 0) {
+            sh.issued[0] = did;
+            const uint32_t there = in_cta(&sh.issued[1], rank ^ 1);
+            pair_store(there + offsetof(PairIssued, full), did.full);
+            pair_store(there + offsetof(PairIssued, values), did.values);
+            pair_store(there + offsetof(PairIssued, last), did.last);
+            pair_store(there + offsetof(PairIssued, used), did.used);
+            pair_store(there + offsetof(PairIssued, queries), did.queries);
+            pair_store(there + offsetof(PairIssued, expects), did.expects);
+            pair_store(there + offsetof(PairIssued, asks), did.asks);
+        }
     } else if (warp == kMmaWarp && rank == 0) {
         constexpr uint32_t id_s = inst_desc(kPairRows, kKeys, false, false), id_o = inst_desc(kPairRows, DV, false, true);
         const uint64_t dq = desc128_k(smem_addr(sm), 1024), dk = desc128_k(smem_addr(s_ring), 1024),
@@ -590,12 +636,23 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             it = then;
         }
     }
-    if (!ok)
+    if (!ok) {
         atomicOr(&g_pairs_status, 1);
+        sh.failed = 1;
+        pair_store(in_cta(&sh.failed, rank ^ 1), 1);
+    }
     pdl_launch_dependents();
     fence_before();
     __syncthreads();
     pair_sync(); // neither CTA leaves while the other's steps or arrivals may reach it
+    if (sh.failed) { // in both CTAs or in neither: copies may be on their way, to phases that nobody has waited for
+        if (warp == kCopyWarp && lane == 0) {
+            DrainBars<S> bars{sh};
+            pair_drain(sh.issued[0], sh.issued[1], rank == 0, S::kSlots, bars);
+        }
+        __syncthreads();
+        pair_sync();
+    }
     if (warp == 0) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
