@@ -424,6 +424,14 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         // what has been issued, for either CTA's last waits
         did.used = uint32_t(to.used);
         if (lane == 0) {
+            // The products' last arrivals come to both CTAs, and only the first, which
+            // issues them, waits for its own: the second may not leave before they are here.
+            if (rank == 1 && ok) {
+                auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && bar_wait(bar, parity); };
+                to.drain([&](int k, uint32_t parity) { wait(&sh.free_[k], parity); });
+                wait(&sh.q_free, (did.queries & 1u) ^ 1u); // (none copied: the phase before the first, ended)
+                wait(&sh.end, 0);
+            }
             sh.issued[0] = did;
             const uint32_t there = in_cta(&sh.issued[1], rank ^ 1);
             pair_store(there + offsetof(PairIssued, full), did.full);

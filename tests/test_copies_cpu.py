@@ -78,9 +78,10 @@ def test_ring_is_drained_wherever_its_reader_stops(tmp_path):
     run(tmp_path, RING)
 
 
-@pytest.mark.parametrize("kernel,rings", [("w8_latent_paged.cu", 2), ("w8_latent_expanded.cu", 1)])
+@pytest.mark.parametrize("kernel,rings", [("w8_latent_paged.cu", 2), ("w8_latent_expanded.cu", 1), ("w8_latent_pair.cu", 1)])
 def test_kernels_drain_their_rings(kernel, rings):
-    """Every ring of a copying lane is drained, whether or not the lane itself gave up."""
+    """Every ring of a copying lane is drained, whether or not the lane itself gave up.  (In a pair the second
+    CTA's lane waits so for the products that read it: their arrivals are the last to reach the CTA.)"""
     text = open(os.path.join(CSRC, kernel)).read()
     assert text.count("Ring<") == rings and text.count(".drain(") == rings
     for part in text.split(".drain(")[:-1]:
