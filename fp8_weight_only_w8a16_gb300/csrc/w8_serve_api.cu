@@ -36,6 +36,20 @@ w8_status check_cache(const w8_latent_cache &c)
     return aligned(c.data, 16) && c.ld_tok % 8 == 0 && c.ld_page % 8 == 0 ? W8_OK : W8_ERR_ALIGN;
 }
 
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+// Whether a range meets one of `rows` rows of `bytes` bytes, `ld` bytes apart.
+bool meets(const Range &a, const void *p, int64_t rows, int64_t ld, int64_t bytes)
+{
+    if (a.bytes <= 0 || bytes <= 0)
+        return false;
+    const int64_t at = int64_t(reinterpret_cast<uintptr_t>(a.p)) - int64_t(reinterpret_cast<uintptr_t>(p)); // from the first row
+    const int64_t row = at < bytes ? 0 : (at - bytes) / ld + 1; // the first row that ends behind the range's start
+    return row < rows && row * ld < at + a.bytes;
+}
+
 // SMs of the current device; 0 on failure.
 int current_sms()
 {
@@ -68,8 +82,8 @@ const char *w8_serve_status_str(w8_status s)
     case W8_ERR_NULL: return "a required pointer is NULL";
     case W8_ERR_DTYPE: return "logits are bf16 or fp32";
     case W8_ERR_SHAPE: return "a count, stride or head shape outside what the function takes "
-                              "(limits: w8_serve.h), or one address for free_head and "
-                              "free_head_out";
+                              "(limits: w8_serve.h), or an output of w8_block_tables on one of "
+                              "its inputs";
     case W8_ERR_SCALE: return "the softmax scale must be finite and above zero";
     case W8_ERR_CAPACITY: return "workspace too small";
     case W8_ERR_ALIGN: return "misaligned operand (bf16 operands: 16 B with strides in multiples "
@@ -110,6 +124,18 @@ w8_status w8_block_tables(const int32_t *ctx_lens, const int32_t *new_lens, int 
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(slots, 8) ||
         !aligned(positions, 4) || !aligned(free_head_out, 4) || !aligned(status, 4))
         return W8_ERR_ALIGN;
+    // Every CTA reads all lengths while others write: no output may lie on an input.
+    const int64_t n = n_req, toks = max_tokens;
+    const Range in[] = {{ctx_lens, 4 * n}, {new_lens, 4 * n}, {free_pages, 4 * int64_t(n_free)}, {free_head, 4}},
+                out[] = {{seq_lens, 4 * n},  {cu_new, 4 * (n + 1)}, {slots, 8 * toks},
+                         {positions, 4 * toks}, {free_head_out, 4},    {status, 4}};
+    for (const Range &i : in) {
+        for (const Range &o : out)
+            if (meets(i, o.p, 1, 1, o.bytes))
+                return W8_ERR_SHAPE;
+        if (meets(i, block_table, n, 4 * ld_table, 4 * int64_t(max_pages)))
+            return W8_ERR_SHAPE;
+    }
     const int sms = current_sms();
     if (sms < 1)
         return W8_ERR_CUDA;

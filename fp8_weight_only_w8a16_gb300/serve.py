@@ -161,7 +161,8 @@ def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_size: int,
                  stream=None) -> None:
     """Take the pages that the appended tokens need from the free list and
     write the tables, lengths, offsets, slots and positions of the step (one
-    kernel launch).  ``status`` is 0 when everything fitted."""
+    kernel launch).  ``status`` is 0 when everything fitted.  No output shares
+    memory with an input: ``seq_lens`` are copied to ``ctx_lens`` afterwards."""
     n, toks = ctx_lens.numel(), slots.numel()
     _check(lib.w8_block_tables(
         _ints(ctx_lens), _ints(new_lens, n=n), n, page_size, _ints(free_pages), free_pages.numel(),

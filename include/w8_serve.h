@@ -87,11 +87,12 @@ w8_status w8_serve_device_status(int *status, int reset);
  *   4: a length below zero (taken as 0), a sequence past 2^31 - 1 tokens (cut
  *      there), or more than max_tokens tokens (those past it get no slot).
  * ctx_lens, new_lens: device int32 [n_req]; free_pages: device int32
- * [n_free]; free_head, free_head_out: device int32, not the same address (a
- * step that is run again gives the same answer); block_table: device int32
+ * [n_free]; free_head, free_head_out: device int32; block_table: device int32
  * [n_req][ld_table], ld_table >= max_pages; seq_lens [n_req], cu_new
  * [n_req + 1], positions [max_tokens]: device int32; slots: device int64
- * [max_tokens]; status: device int32.
+ * [max_tokens]; status: device int32.  No output may lie on an input (lengths
+ * are not advanced in place, a step that is run again gives the same answer):
+ * W8_ERR_SHAPE.
  * 1 <= n_req <= W8_MAX_REQUESTS, max_pages >= 1, max_tokens >= 0,
  * 1 <= page_size <= 2^20.  One kernel launch. */
 w8_status w8_block_tables(const int32_t *ctx_lens, const int32_t *new_lens, int n_req, int page_size,

@@ -61,3 +61,44 @@ def test_one_token_at_an_odd_place(serve):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert torch.equal(got[0][2], v[0])  # the only key's value
+
+
+def test_lengths_are_not_advanced_in_place(serve):
+    """Every CTA reads all lengths while the first writes the new ones."""
+    n = 3000
+    ctx, new, free = i32([5] * n), i32([1] * n), i32(range(9))
+    table, seq, cu = torch.full((n, 2), 3, dtype=torch.int32, device="cuda"), i32([0] * n), i32([0] * (n + 1))
+    slots, pos, head = torch.zeros(n, dtype=torch.int64, device="cuda"), i32([0] * n), i32([0])
+    for kw in (dict(seq_lens=ctx), dict(seq_lens=new), dict(positions=ctx)):
+        with pytest.raises(serve.W8Error):
+            serve.block_tables(ctx, new, 16, free, head, table, **{**dict(seq_lens=seq, positions=pos), **kw}, cu_new=cu,
+                               slots=slots, free_head_out=i32([0]), status=i32([0]))
+    torch.cuda.synchronize()
+    assert (ctx == 5).all() and (new == 1).all() and (table == 3).all()
+
+
+def test_tables_buffers_side_by_side(serve):
+    """Inputs and outputs cut from one buffer, none on another, also between the table's rows."""
+    n, width, ld = 300, 3, 8
+    lens = torch.zeros(6 * n + 20, dtype=torch.int32, device="cuda")
+    at = 0
+
+    def cut(k):
+        nonlocal at
+        at += k
+        return lens[at - k:at]
+
+    ctx, seq, new, cu, free, head, out, status = (cut(k) for k in (n, n, n, n + 1, n, 1, 1, 1))
+    ctx.fill_(16)
+    new.fill_(1)
+    free.copy_(torch.arange(n))
+    pos, slots = i32([0] * n), torch.zeros(n, dtype=torch.int64, device="cuda")
+    table = torch.full((n, ld), -7, dtype=torch.int32, device="cuda")
+    serve.block_tables(ctx, new, 16, free, head, table[:, :width], seq, cu, slots, pos, out, status)
+    assert int(status) == 0 and int(out) == n and (seq == 17).all() and torch.equal(cu, torch.arange(n + 1, device="cuda").int())
+    assert torch.equal(table[:, 1], torch.arange(n, device="cuda").int()) and (table[:, 2:] == -7).all()
+    assert torch.equal(slots, torch.arange(n, device="cuda") * 16)
+    # one request's length in the gap behind its table row
+    row = torch.tensor([[-7, -7, -7, 16, -7]], dtype=torch.int32, device="cuda")
+    serve.block_tables(row[0, 3:4], new[:1], 16, free, head, row[:, :3], seq[:1], cu[:2], slots[:1], pos[:1], out, status)
+    assert row.tolist() == [[-7, 0, -7, 16, -7]] and int(status) == 0

@@ -183,3 +183,34 @@ def test_the_stride_of_one_entry_says_nothing(calls):
     assert fields[1:3] == (384, 128) and fields[4:6] == (192, 64) and fields[7:9] == (384, 128) and fields[10] == 64
     assert d[1] == 512 and d[3] == 64
     assert pack(e[0])[1:3] == (512, 512) and pack(e[0])[7:9] == (16 * 576, 576)
+
+
+# ---------------------------------------------------------------------------
+# outputs of the bookkeeping that lie on its inputs: refused before any CUDA call
+# ---------------------------------------------------------------------------
+
+N, FREE, TOKS, WIDTH, LD = 2000, 700, 3000, 20, 40
+BUFFERS = dict(ctx=4 * N, new=4 * N, free=4 * FREE, head=4, table=4 * ((N - 1) * LD + WIDTH), seq=4 * N, cu=4 * (N + 1),
+               slots=8 * TOKS, pos=4 * TOKS, out=4, status=4)
+PLACES = {name: 0x1000000 * (i + 1) for i, name in enumerate(BUFFERS)}
+INPUTS, OUTPUTS = ("ctx", "new", "free", "head"), ("table", "seq", "cu", "slots", "pos", "out", "status")
+
+
+def on_inputs():
+    for i in INPUTS:
+        for o in OUTPUTS:
+            step = 8 if o == "slots" else 4
+            last = BUFFERS[o] - step
+            yield i, o, PLACES[i]                                    # the same address
+            yield i, o, (PLACES[i] - last) // step * step            # the output's last entry on the input's first
+            yield i, o, (PLACES[i] + BUFFERS[i] - 4) // step * step  # its first on the input's last
+            if o == "table":  # a row in the middle
+                yield i, o, PLACES[i] - 4 * LD * 1000 - 4 * (WIDTH - 1)
+
+
+@pytest.mark.parametrize("i,o,at", list(on_inputs()))
+def test_tables_outputs_on_inputs_are_refused(i, o, at):
+    p = {**PLACES, o: at}
+    got = serve.lib.w8_block_tables(p["ctx"], p["new"], N, 16, p["free"], FREE, p["head"], p["table"], LD, WIDTH, p["seq"],
+                                    p["cu"], p["slots"], p["pos"], TOKS, p["out"], p["status"], None)
+    assert serve.w8.STATUS[got] == "W8_ERR_SHAPE"
