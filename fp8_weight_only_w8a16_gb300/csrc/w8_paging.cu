@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
     // fresh table entries: a warp a request, the requests dealt over all CTAs
     for (int r = blockIdx.x * warps + warp; r < a.n_req; r += gridDim.x * warps) {
         const int32_t ctx = s_ctx[r], base = s_base[r];
-        const int64_t fresh = s_cu[r + 1] - s_cu[r];
+        // (not from the offsets: they are cut at the end of the number range)
+        const int64_t fresh = min(max(__ldg(a.fresh + r), 0), INT32_MAX - ctx);
         const int have = int((int64_t(ctx) + a.page - 1) / a.page);
         const int want = int(min((ctx + fresh + a.page - 1) / a.page, int64_t(a.max_pages)));
         for (int p = have + lane; p < want; p += 32) {

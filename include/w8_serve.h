@@ -71,6 +71,7 @@ w8_status w8_serve_device_status(int *status, int reset);
  * both cut at max_pages, and base_r = *free_head + sum_{r' < r} (want - have):
  *   block_table[r][p] = free_pages[base_r + p - have_r],  have_r <= p < want_r
  *   seq_lens[r] = ctx + new,   cu_new[r] = sum_{r' < r} new,  cu_new[n_req] = all
+ *   (the sums cut at 2^31 - 1)
  *   for token t of request r, pos = ctx_r + t - cu_new[r]:
  *     positions[t] = pos,
  *     slots[t] = block_table[r][pos / page_size] * page_size + pos % page_size

@@ -113,6 +113,22 @@ def test_tables_bad_lengths_are_flagged(serve):
     assert got[1] == [2 ** 31 - 1] and got[-1] == 6 and got[3] == [-1] * 4 and got[5] == 0
 
 
+@pytest.mark.parametrize("at", [0, 1, 3])
+def test_tables_behind_a_sum_that_is_cut(serve, at):
+    """A length that takes the sum of tokens past the number range: the requests behind it still get their
+    pages written, each page that is taken off the list."""
+    page, width = 1 << 20, 3
+    ctx, new = [0, 5, page, page - 1, 2 * page], [3, 4, 2, page, 7]
+    new[at] = 2 ** 31 - 1 - ctx[at]
+    new[4] = 2 ** 31 - 1 - ctx[4] if at == 3 else new[4]
+    table = [[40 + 3 * r + p if p < -(-c // page) else -5 for p in range(width)] for r, c in enumerate(ctx)]
+    args = (ctx, new, page, list(range(100, 120)), 2, table, 9)
+    want = list(tables_plain(*args))
+    want[2] = [min(c, 2 ** 31 - 1) for c in want[2]]
+    assert run_tables(serve, *args) == tuple(want)
+    assert want[-1] == 6 and not any(-5 in row for r, row in enumerate(want[0]) if r == at)
+
+
 def test_tables_slots_pass_32_bits(serve):
     page = 1 << 20
     got = run_tables(serve, [5], [3], page, [1], 0, [[2 ** 31 - 1, -5]], 3)
