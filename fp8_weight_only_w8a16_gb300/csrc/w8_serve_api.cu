@@ -97,6 +97,9 @@ w8_status w8_serve_device_status(int *status, int reset)
 {
     if (!status)
         return W8_ERR_NULL;
+    // all streams' launches so far: the copies below wait for none that does not block
+    if (cudaDeviceSynchronize() != cudaSuccess)
+        return W8_ERR_CUDA;
     int paged = 0, expanded = 0, pairs = 0;
     if (w8::paged_status(&paged, reset != 0) != cudaSuccess || w8::expanded_status(&expanded, reset != 0) != cudaSuccess ||
         w8::pairs_status(&pairs, reset != 0) != cudaSuccess)

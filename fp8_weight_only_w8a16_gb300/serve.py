@@ -81,7 +81,7 @@ def status_str(status: int) -> str:
 
 def device_status(reset: bool = False) -> int:
     """The attention kernels' status word on the current device (0: every
-    bounded wait ended normally).  Synchronous."""
+    bounded wait ended normally).  Synchronous with all streams."""
     out = ctypes.c_int(0)
     _check(lib.w8_serve_device_status(ctypes.byref(out), 1 if reset else 0))
     return int(out.value)

@@ -61,7 +61,8 @@ const char *w8_serve_status_str(w8_status s);
 /* The status word of the attention kernels on the current device: 0 when every
  * bounded wait of every launch so far ended normally; otherwise bit 0 (paged
  * form) or bit 1 (expanded form) is set and the outputs of some launch are
- * wrong.  Synchronous; reset != 0 clears it. */
+ * wrong.  Synchronous: it waits for all work of the device, whatever its
+ * stream; reset != 0 clears the word. */
 w8_status w8_serve_device_status(int *status, int reset);
 
 /* ---------------------------------------------------------------------------

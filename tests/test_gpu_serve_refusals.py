@@ -1,6 +1,6 @@
 """GPU tests of what the serving operators refuse when they are called as a user
-calls them: a W8Error before anything is enqueued, and the outputs untouched; and of calls that
-look odd and are not refused."""
+calls them: a W8Error before anything is enqueued, and the outputs untouched; of calls that
+look odd and are not refused; and of what the status call waits for."""
 from __future__ import annotations
 
 import pytest
@@ -102,3 +102,17 @@ def test_tables_buffers_side_by_side(serve):
     row = torch.tensor([[-7, -7, -7, 16, -7]], dtype=torch.int32, device="cuda")
     serve.block_tables(row[0, 3:4], new[:1], 16, free, head, row[:, :3], seq[:1], cu[:2], slots[:1], pos[:1], out, status)
     assert row.tolist() == [[-7, 0, -7, 16, -7]] and int(status) == 0
+
+
+@pytest.mark.parametrize("reset", [False, True])
+def test_device_status_waits_for_every_stream(serve, reset):
+    """A wait that gives up sets the word when its launch runs: the call waits for launches of streams that
+    do not block, as torch's own do not."""
+    torch.cuda.synchronize()
+    done, side = torch.cuda.Event(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+        done.record()
+    assert not done.query()
+    assert serve.device_status(reset=reset) == 0
+    assert done.query()
