@@ -239,7 +239,8 @@ w8_status w8_device_status(int *status, int reset)
 {
     if (!status)
         return W8_ERR_NULL;
-    if (w8::tc_status(status, reset != 0) != cudaSuccess)
+    // (the copy alone waits for no stream that does not block)
+    if (cudaDeviceSynchronize() != cudaSuccess || w8::tc_status(status, reset != 0) != cudaSuccess)
         return W8_ERR_CUDA;
     return W8_OK;
 }

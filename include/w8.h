@@ -226,7 +226,8 @@ typedef struct w8_build w8_build; /* opaque, host-side, library-owned */
  * wait of every launch so far ended normally; bit 0 = a pipeline-stage wait
  * gave up, bit 1 = the accumulator wait gave up (each wait polls a bounded
  * number of times, then the kernel runs to its end with that output wrong and
- * flags it here).  Synchronous (reads device memory); reset != 0 clears it.
+ * flags it here).  Synchronous (waits for all work of the device, whatever its
+ * stream, and reads device memory); reset != 0 clears it.
  * No counterpart on the pages: it reports this library's own safety bound. */
 w8_status w8_device_status(int *status, int reset);
 

@@ -105,7 +105,8 @@ def test_tables_buffers_side_by_side(serve):
 
 
 @pytest.mark.parametrize("reset", [False, True])
-def test_device_status_waits_for_every_stream(serve, reset):
+@pytest.mark.parametrize("module", ["serve", "w8"])
+def test_device_status_waits_for_every_stream(serve, module, reset):
     """A wait that gives up sets the word when its launch runs: the call waits for launches of streams that
     do not block, as torch's own do not."""
     torch.cuda.synchronize()
@@ -114,5 +115,5 @@ def test_device_status_waits_for_every_stream(serve, reset):
         torch.cuda._sleep(100_000_000)  # some 50 ms
         done.record()
     assert not done.query()
-    assert serve.device_status(reset=reset) == 0
+    assert (serve if module == "serve" else serve.w8).device_status(reset=reset) == 0
     assert done.query()
