@@ -107,17 +107,22 @@ class LatentLayer:
 
     def step(self, q_c: torch.Tensor, kv_a: torch.Tensor, new_lens: torch.Tensor, prompt: bool):
         """The greedy next token of every request, its log probability, the entropy and
-        the five likeliest tokens with theirs."""
-        rows = new_lens.numel()
+        the five likeliest tokens with theirs.  A request that appends nothing has no
+        next token: -1, and NaN for the values."""
+        rows, idle = new_lens.numel(), new_lens <= 0
         hidden = self.project(2, self.attention(q_c, kv_a, new_lens, prompt), self.hidden)
-        logits = torch.empty(rows, self.vocab, dtype=torch.bfloat16, device="cuda")
-        w8.bf16_gemv(self.head, 0, hidden[self.cu[1:].long() - 1], logits, self.head_ws)
-        tokens = logits.argmax(1).to(torch.int32)
+        logits = torch.zeros(rows, self.vocab, dtype=torch.bfloat16, device="cuda")
+        if hidden.shape[0] > 0:
+            # each request's last token (an idle one's place holds another's, or lies before the first)
+            w8.bf16_gemv(self.head, 0, hidden[(self.cu[1:].long() - 1).clamp(min=0)], logits, self.head_ws)
+        tokens = logits.argmax(1).to(torch.int32).masked_fill_(idle, -1)
         logprob, entropy = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
         ids = torch.empty(rows, 5, dtype=torch.int32, device="cuda")
         tops = torch.empty(rows, 5, device="cuda")
         serve.token_logprobs(logits, tokens, logprob, entropy, ids, tops, self.logprob_ws)
-        return tokens, logprob, entropy, ids, tops
+        nan = float("nan")
+        return (tokens, logprob, entropy.masked_fill_(idle, nan), ids.masked_fill_(idle[:, None], -1),
+                tops.masked_fill_(idle[:, None], nan))
 
 
 def main():

@@ -47,3 +47,49 @@ def test_decoded_tokens_match_the_prompt():
     assert torch.equal(ids[:, 0], tokens) and torch.equal(tops[:, 0], logprob)
     assert (logprob < 0).all() and (entropy > 0).all() and (tops[:, :-1] >= tops[:, 1:]).all()
     assert serve.device_status() == 0 and w8.device_status() == 0
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def small_layer(**kw):
+    from fp8_weight_only_w8a16_gb300 import latent_step
+    return latent_step.LatentLayer(**{**dict(heads=16, hidden=512, q_rank=256, vocab=1000, requests=4, pages=40, page=16, seed=3), **kw})
+
+
+def activations(toks, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(toks, 256, generator=g, device="cuda").to(torch.bfloat16),
+            torch.randn(toks, 576, generator=g, device="cuda").to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("new", [[0, 2, 1, 3], [1, 0, 0, 2], [2, 1, 0, 0], [0, 0, 0, 1], [0, 0, 0, 0], [1, 2, 1, 1]])
+def test_requests_that_append_nothing(new):
+    """Each request's tokens come from its own last row of the attention output, whichever requests are idle:
+    bit for bit what the projections and the log probabilities give for those rows.  An idle request gets
+    -1 and NaN."""
+    from fp8_weight_only_w8a16_gb300 import serve, w8
+    layer = small_layer()
+    layer.step(*activations(90, 5), i32([20, 30, 7, 33]), True)
+    q_c, kv_a = activations(sum(new), 6)
+    attention, seen = layer.attention, []
+    layer.attention = lambda *args: seen.append(attention(*args)) or seen[0]
+    tokens, logprob, entropy, ids, tops = layer.step(q_c, kv_a, i32(new), False)
+    live = [r for r in range(4) if new[r]]
+    idle = [r for r in range(4) if not new[r]]
+    assert (tokens[idle] == -1).all() and (ids[idle] == -1).all()
+    for values in (logprob, entropy, tops):
+        assert torch.isnan(values[idle]).all() and torch.isfinite(values[live]).all()
+    if live:
+        hidden = layer.project(2, seen[0], layer.hidden)
+        ends = [max(sum(new[:r + 1]) - 1, 0) for r in range(4)]
+        logits = torch.empty(4, 1000, dtype=torch.bfloat16, device="cuda")
+        w8.bf16_gemv(layer.head, 0, hidden[ends], logits, layer.head_ws)
+        want = logits.argmax(1).to(torch.int32)
+        lp, ent = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+        top, top_lp = torch.empty(4, 5, dtype=torch.int32, device="cuda"), torch.empty(4, 5, device="cuda")
+        serve.token_logprobs(logits, want, lp, ent, top, top_lp, serve.new_logprobs_workspace(4, 1000, 5))
+        for got, ref in ((tokens, want), (logprob, lp), (entropy, ent), (ids, top), (tops, top_lp)):
+            assert torch.equal(got[live], ref[live])
+    assert serve.device_status() == 0 and w8.device_status() == 0
