@@ -80,12 +80,21 @@ class LatentLayer:
 
     def attention(self, q_c: torch.Tensor, kv_a: torch.Tensor, new_lens: torch.Tensor, prompt: bool):
         """The attention output [T, heads * 256] of the step's tokens: q_c [T, q_rank],
-        kv_a [T, 576] (the latent and the key to be rotated), new_lens tokens a request."""
+        kv_a [T, 576] (the latent and the key to be rotated), new_lens tokens a request.
+        A step that does not fit -- pages, table rows, or other than T tokens in all -- is
+        refused and leaves the layer as it was; to know, it waits for the lengths."""
         toks, heads = q_c.shape[0], self.heads
+        if kv_a.shape[0] != toks or new_lens.numel() != self.ctx.numel():
+            raise ValueError("kv_a has a row a token, new_lens an entry a request")
         slots = torch.empty(toks, dtype=torch.int64, device="cuda")
         positions = torch.empty(toks, dtype=torch.int32, device="cuda")
         serve.block_tables(self.ctx, new_lens, self.page, self.free, self.free_head, self.table, self.seq_lens,
                            self.cu, slots, positions, self.next_head, self.status)
+        status, total = torch.cat([self.status, self.cu[-1:]]).tolist()
+        if status or total != toks:
+            raise ValueError(f"{total} new tokens for {toks} rows" if total != toks else
+                             "a length below zero" if status & 4 else
+                             "no free page is left" if status & 1 else "a request outgrows its table row")
         self.free_head, self.next_head = self.next_head, self.free_head
         self.ctx.copy_(self.seq_lens)
         latent, k_rope = kv_a[:, :LATENT], rotate(kv_a[:, LATENT:], positions)
@@ -139,7 +148,7 @@ def main():
         print(f"{'prompt' if prompt else 'decode'} {lens}: tokens {tokens.tolist()} "
               f"log p {[round(v, 3) for v in logprob.tolist()]} entropy {[round(v, 3) for v in entropy.tolist()]} "
               f"top {ids[:, :3].tolist()}")
-    assert int(layer.status) == 0 and serve.device_status() == 0 and w8.device_status() == 0
+    assert serve.device_status() == 0 and w8.device_status() == 0
 
 
 if __name__ == "__main__":

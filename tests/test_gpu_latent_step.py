@@ -93,3 +93,35 @@ def test_requests_that_append_nothing(new):
         for got, ref in ((tokens, want), (logprob, lp), (entropy, ent), (ids, top), (tops, top_lp)):
             assert torch.equal(got[live], ref[live])
     assert serve.device_status() == 0 and w8.device_status() == 0
+
+
+@pytest.mark.parametrize("layer,first,new,toks", [
+    (dict(pages=5), [20, 16, 0, 1], [0, 0, 17, 0], 17),       # no page left
+    (dict(pages=40), [20, 16, 0, 1], [1, 1, 1, 1], 3),        # more tokens than rows,
+    (dict(pages=40), [20, 16, 0, 1], [1, 1, 1, 1], 5),        # fewer,
+    (dict(pages=40), [20, 16, 0, 1], [1, -1, 1, 1], 3),       # a length below zero
+    (dict(pages=4), [20, 0, 0, 0], [50, 0, 0, 0], 50)])       # a table row outgrown
+def test_a_step_that_does_not_fit_is_refused(layer, first, new, toks):
+    """... and leaves the layer as it was: the next step that fits gives what it gives without it."""
+    from fp8_weight_only_w8a16_gb300 import serve, w8
+    layers = [small_layer(**layer) for _ in range(2)]
+    for l in layers:
+        l.step(*activations(sum(first), 7), i32(first), True)
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            layers[0].step(*activations(toks, 8), i32(new), False)
+    assert layers[0].ctx.tolist() == first
+    got = [l.step(*activations(3, 9), i32([2, 0, 0, 1]), False) for l in layers]
+    for a, b in zip(*got):
+        assert torch.equal(a[[0, 3]], b[[0, 3]])
+    assert torch.equal(layers[0].ctx, layers[1].ctx) and torch.equal(layers[0].free_head, layers[1].free_head)
+    assert serve.device_status() == 0 and w8.device_status() == 0
+
+
+def test_rows_and_requests_are_counted():
+    layer = small_layer()
+    q_c, kv_a = activations(4, 10)
+    with pytest.raises(ValueError):
+        layer.step(q_c, kv_a[:3], i32([1, 1, 1, 1]), True)
+    with pytest.raises(ValueError):
+        layer.step(q_c, kv_a, i32([1, 1, 2]), True)
