@@ -80,7 +80,8 @@ class LatentLayer:
 
     def attention(self, q_c: torch.Tensor, kv_a: torch.Tensor, new_lens: torch.Tensor, prompt: bool):
         """The attention output [T, heads * 256] of the step's tokens: q_c [T, q_rank],
-        kv_a [T, 576] (the latent and the key to be rotated), new_lens tokens a request.
+        kv_a [T, 576] (the latent and the key to be rotated), new_lens tokens a request;
+        prompt: the step is its requests' first, and they attend to its own tokens alone.
         A step that does not fit -- pages, table rows, or other than T tokens in all -- is
         refused and leaves the layer as it was; to know, it waits for the lengths."""
         toks, heads = q_c.shape[0], self.heads
@@ -90,7 +91,10 @@ class LatentLayer:
         positions = torch.empty(toks, dtype=torch.int32, device="cuda")
         serve.block_tables(self.ctx, new_lens, self.page, self.free, self.free_head, self.table, self.seq_lens,
                            self.cu, slots, positions, self.next_head, self.status)
-        status, total = torch.cat([self.status, self.cu[-1:]]).tolist()
+        cached = ((self.ctx > 0) & (new_lens > 0)).any().to(torch.int32)[None]
+        status, total, cached = torch.cat([self.status, self.cu[-1:], cached]).tolist()
+        if prompt and cached:
+            raise ValueError("a prompt's requests have nothing cached")
         if status or total != toks:
             raise ValueError(f"{total} new tokens for {toks} rows" if total != toks else
                              "a length below zero" if status & 4 else

@@ -125,3 +125,15 @@ def test_rows_and_requests_are_counted():
         layer.step(q_c, kv_a[:3], i32([1, 1, 1, 1]), True)
     with pytest.raises(ValueError):
         layer.step(q_c, kv_a, i32([1, 1, 2]), True)
+
+
+def test_a_prompt_has_nothing_cached():
+    """The expanded form sees the step's own tokens only: a request that has more is not a prompt's."""
+    layer = small_layer()
+    layer.step(*activations(30, 11), i32([20, 10, 0, 0]), True)
+    with pytest.raises(ValueError):
+        layer.step(*activations(3, 12), i32([0, 2, 0, 1]), True)
+    assert layer.ctx.tolist() == [20, 10, 0, 0]
+    # requests that start beside idle ones are
+    tokens = layer.step(*activations(3, 12), i32([0, 0, 2, 1]), True)[0]
+    assert layer.ctx.tolist() == [20, 10, 2, 1] and (tokens[:2] == -1).all() and (tokens[2:] >= 0).all()
