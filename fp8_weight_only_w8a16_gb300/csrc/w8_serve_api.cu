@@ -292,6 +292,24 @@ w8_status w8_logprobs_workspace_bytes(int n_rows, int vocab, int top, int sm_cou
     return W8_OK;
 }
 
+w8_status w8_logprobs_workspace_bytes_upto(int n_rows, int vocab, int top, int sm_count, size_t *bytes)
+{
+    size_t most = 0;
+    const w8_status st = w8_logprobs_workspace_bytes(n_rows, vocab, top, sm_count, bytes);
+    if (st != W8_OK)
+        return st;
+    // Fewer rows are cut into more runs each, and may need more than many that are
+    // not cut; a smaller vocabulary never needs more.
+    for (int rows = 1; rows <= n_rows; ++rows) {
+        const size_t need = logprobs_ws_bytes(rows, vocab, sm_count);
+        if (need == 0) // nor do more rows
+            break;
+        most = need > most ? need : most;
+    }
+    *bytes = most;
+    return W8_OK;
+}
+
 w8_status w8_token_logprobs(const void *logits, int dtype, int64_t ld, int n_rows, int vocab,
                             const int32_t *tokens, float *logprob, float *entropy, int top,
                             int32_t *top_ids, float *top_logprobs, void *workspace,

@@ -22,7 +22,7 @@ from .w8 import W8Error
 LATENT_DIM, LATENT_ROPE, LATENT_ROW = 512, 64, 576
 MAX_REQUESTS, MAX_LATENT_HEADS, MAX_TOP = 16384, 256, 32
 LOGITS_BF16, LOGITS_F32 = 1, 2
-SERVE_ABI_VERSION = 1  # W8_SERVE_ABI_VERSION of include/w8_serve.h
+SERVE_ABI_VERSION = 2  # W8_SERVE_ABI_VERSION of include/w8_serve.h
 
 lib = w8.lib
 
@@ -30,7 +30,7 @@ lib = w8.lib
 EXPORTS = ("w8_serve_abi_version", "w8_serve_status_str", "w8_serve_device_status",
            "w8_block_tables", "w8_latent_cache_write", "w8_latent_attn_paged",
            "w8_latent_paged_workspace_bytes", "w8_latent_attn_expanded", "w8_token_logprobs",
-           "w8_logprobs_workspace_bytes")
+           "w8_logprobs_workspace_bytes", "w8_logprobs_workspace_bytes_upto")
 
 # the structs of w8_serve.h, packed field by field (native sizes and padding)
 _CACHE = struct.Struct("@Pqqii")
@@ -62,6 +62,8 @@ def _load():
     lib.w8_token_logprobs.restype = st
     lib.w8_logprobs_workspace_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
     lib.w8_logprobs_workspace_bytes.restype = st
+    lib.w8_logprobs_workspace_bytes_upto.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.w8_logprobs_workspace_bytes_upto.restype = st
     if lib.w8_serve_abi_version() != SERVE_ABI_VERSION:
         raise ImportError(f"{w8.LIB_PATH} has serving ABI {lib.w8_serve_abi_version()}, this "
                           f"binding {SERVE_ABI_VERSION}: rebuild it")
@@ -242,11 +244,17 @@ def logprobs_workspace_bytes(n_rows: int, vocab: int, top: int, sm_count: int) -
     return int(out.value)
 
 
+def logprobs_workspace_bytes_upto(n_rows: int, vocab: int, top: int, sm_count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.w8_logprobs_workspace_bytes_upto(n_rows, vocab, top, sm_count, ctypes.byref(out)))
+    return int(out.value)
+
+
 def new_logprobs_workspace(n_rows: int, vocab: int, top: int = 0, device=None) -> torch.Tensor:
-    """A zero-filled workspace for token_logprobs calls of this shape (its
-    counters must start at zero)."""
+    """A zero-filled workspace for token_logprobs calls of up to these counts
+    (its counters must start at zero)."""
     device = _device(device)
-    nbytes = logprobs_workspace_bytes(n_rows, vocab, top, _sms(device))
+    nbytes = logprobs_workspace_bytes_upto(n_rows, vocab, top, _sms(device))
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 

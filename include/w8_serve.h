@@ -38,7 +38,7 @@
 extern "C" {
 #endif
 
-#define W8_SERVE_ABI_VERSION 1
+#define W8_SERVE_ABI_VERSION 2
 
 /* Columns of a latent-cache row: the latent, then the rope key shared by all
  * heads (kv_a_proj_with_mqa's 576 rows). */
@@ -243,9 +243,9 @@ w8_status w8_latent_attn_expanded(const w8_latent_expanded *a, w8_stream s);
  * entropy: device fp32 [n_rows]; top_ids int32 and top_logprobs fp32
  * [n_rows][top], NULL when top is 0.  0 <= top <= min(W8_MAX_TOP, vocab).
  * n_rows = 0 is a no-op.
- * workspace: w8_logprobs_workspace_bytes bytes, 256-byte aligned, zero-filled
- * once before its first use; every call leaves its counters at zero again;
- * calls that share one must not overlap on the GPU.  One kernel launch. */
+ * workspace: w8_logprobs_workspace_bytes bytes or more, 256-byte aligned,
+ * zero-filled once before its first use; every call, whatever its shape, leaves
+ * its counters at zero again; calls that share one must not overlap on the GPU.  One kernel launch. */
 #define W8_LOGITS_BF16 1
 #define W8_LOGITS_F32 2
 w8_status w8_token_logprobs(const void *logits, int dtype, int64_t ld, int n_rows, int vocab,
@@ -253,8 +253,13 @@ w8_status w8_token_logprobs(const void *logits, int dtype, int64_t ld, int n_row
                             int32_t *top_ids, float *top_logprobs, void *workspace,
                             size_t workspace_bytes, w8_stream s);
 
-/* Workspace bytes of such a call on a GPU of sm_count SMs (host-only). */
+/* Workspace bytes of such a call on a GPU of sm_count SMs (host-only).  They do
+ * not grow with the rows: many rows need none. */
 w8_status w8_logprobs_workspace_bytes(int n_rows, int vocab, int top, int sm_count, size_t *bytes);
+
+/* Workspace bytes that serve every call of up to n_rows rows, vocab columns and
+ * top alternatives (host-only). */
+w8_status w8_logprobs_workspace_bytes_upto(int n_rows, int vocab, int top, int sm_count, size_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -173,6 +173,14 @@ def test_one_workspace_for_many_shapes(serve):
         check(serve, x, tok, top, ws)
 
 
+@pytest.mark.parametrize("most", [305, 700, 9000])
+def test_a_workspace_for_many_rows_serves_fewer(serve, most):
+    ws = serve.new_logprobs_workspace(most, 40000, 8)
+    for rows in (1, 2, 150, 304, most):
+        x, tok = logits(rows, 40000, torch.bfloat16, rows)
+        check(serve, x, tok, 8, ws)
+
+
 def test_same_answer_every_time_and_in_a_graph(serve):
     x, tok = logits(6, 154880, torch.bfloat16, 77)
     first = run(serve, x, tok, 20)

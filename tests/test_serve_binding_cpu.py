@@ -214,3 +214,32 @@ def test_tables_outputs_on_inputs_are_refused(i, o, at):
     got = serve.lib.w8_block_tables(p["ctx"], p["new"], N, 16, p["free"], FREE, p["head"], p["table"], LD, WIDTH, p["seq"],
                                     p["cu"], p["slots"], p["pos"], TOKS, p["out"], p["status"], None)
     assert serve.w8.STATUS[got] == "W8_ERR_SHAPE"
+
+
+@pytest.mark.parametrize("sms", [1, 132, 152])
+@pytest.mark.parametrize("vocab", [1, 4097, 32003, 154880])
+def test_a_workspace_serves_every_smaller_call(sms, vocab):
+    """Fewer rows need more bytes than many: a workspace is sized for the worst of them."""
+    need = [0] + [serve.logprobs_workspace_bytes(r, vocab, 1, sms) for r in range(1, 1400)]
+    worst = 0
+    for r in range(1, 1400):
+        worst = max(worst, need[r])
+        assert serve.logprobs_workspace_bytes_upto(r, vocab, 1, sms) == worst
+    for smaller in (1, 100, 4096, 5000, 30000, 100000):
+        if smaller < vocab:
+            for r in (1, 2, 37, 300, 1399):
+                assert serve.logprobs_workspace_bytes(r, smaller, 1, sms) <= serve.logprobs_workspace_bytes_upto(r, vocab, 1, sms)
+    with pytest.raises(serve.W8Error):
+        serve.logprobs_workspace_bytes_upto(-1, vocab, 0, sms)
+
+
+def test_new_workspaces_serve_every_smaller_call(monkeypatch):
+    class Properties:
+        multi_processor_count = 152
+
+    made = []
+    monkeypatch.setattr(torch.cuda, "get_device_properties", lambda device: Properties)
+    monkeypatch.setattr(torch, "zeros", lambda n, **kw: made.append(n))
+    for rows in (1, 304, 305, 9000):
+        serve.new_logprobs_workspace(rows, 154880, 5, device=0)
+        assert made[-1] >= max(serve.logprobs_workspace_bytes(r, 154880, 5, 152) for r in range(1, rows + 1))
