@@ -83,6 +83,7 @@ constexpr int kPagedThreads = 384, kSoftThreads = 256, kCopyWarp = 8, kScoreWarp
 constexpr int kMaxSlots = 3;
 constexpr int kSmem = 227 * 1024 - 2048;     // what the CTA takes; the rest is static
 constexpr int kTmemCols = 512;
+constexpr int kSeveral = 128;                // above any count of rows, see paged_kernel
 constexpr int kBegin = 2;                    // places of a group's begin in the line
 constexpr float kRaise = 8.0f;               // log2 of how far a row's weights may pass 1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -454,7 +455,60 @@ __device__ __forceinline__ bool query_role(const w8_latent_paged &a, Walk w, uin
 }
 
 // ---- softmax, output --------------------------------------------------------
-template <int NR>
+// A pair of bf16 values with zeros for those that are not finite.
+__device__ __forceinline__ uint32_t finite2(uint32_t u)
+{
+    u = (u & 0x7F80u) == 0x7F80u ? u & 0xFFFF0000u : u;
+    return (u & 0x7F800000u) == 0x7F800000u ? u & 0xFFFFu : u;
+}
+// Zeros for values that are not finite in rows `from` .. of a tile's latents, `vecs`
+// 16-byte vectors a chunk, once the two halves are here: 1 if there were any among
+// this thread's, -1 if a wait gave up.
+__device__ __noinline__ int clear_hidden(uint64_t *front_full, uint32_t front_parity, uint8_t *front, uint64_t *back_full,
+                                         uint32_t back_parity, uint8_t *back, int from, int vecs, int tid)
+{
+    if (!bar_wait(front_full, front_parity) || !bar_wait(back_full, back_parity))
+        return -1;
+    int found = 0;
+    for (int i = tid; i < 8 * vecs; i += kSoftThreads) {
+        const int c = i / vecs, rest = i - c * vecs;
+        uint4 *at = reinterpret_cast<uint4 *>((c < kFront ? front + c * kChunk : back + (c - kFront) * kChunk) + from * 128 + rest * 16);
+        const uint4 u = *at, v = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
+        if (u.x != v.x || u.y != v.y || u.z != v.z || u.w != v.w) {
+            *at = v;
+            found = 1;
+        }
+    }
+    return found;
+}
+// NaN in the outputs of a run's rows (row0 .., `rows` of them) that see a value that
+// is not finite in the request's tokens from .. to - 1: in `out` at the rows' places,
+// or in the run's part.
+__device__ __noinline__ void poison(const w8_latent_paged &a, int r, int row0, int rows, int from, int to, const int64_t *places,
+                                    float *part, int tid)
+{
+    const Request q = request_of(a, r);
+    const int page = a.cache.page_size, shift = 31 - __clz(page);
+    for (int j = from; j < to; ++j) {
+        const int p = __ldg(a.block_table + r * a.ld_table + (j >> shift));
+        if (p < 0 || p >= a.cache.n_pages) // reads as zeros
+            continue;
+        const uint16_t *at = static_cast<const uint16_t *>(a.cache.data) + p * a.cache.ld_page + (j & (page - 1)) * a.cache.ld_tok;
+        for (int d = tid; d < W8_LATENT_DIM; d += kSoftThreads)
+            if ((__ldg(at + d) & 0x7F80u) == 0x7F80u)
+                for (int i = 0; i < rows; ++i)
+                    if (j < seen(q, token_of(q, a.n_heads, row0 + i))) {
+                        if (part)
+                            part[i * W8_LATENT_DIM + d] = CUDART_NAN_F;
+                        else
+                            a.out[places[i] + d] = 0x7FFF;
+                    }
+    }
+}
+// kMixed: groups may hold rows of several query tokens, which do not see the same.
+// (Code of its own, since it slows a tile: 24 requests of 1 to 4 query tokens at 64
+// heads, whose groups are never mixed, 74.6 us with it against 72.4.)
+template <int NR, bool kMixed>
 __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, uint8_t *sm, Shared &sh, uint32_t tmem,
                                              uint32_t tm_s, const Parts &parts, int64_t total, int64_t ctas, int tid)
 {
@@ -477,6 +531,16 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
     for (bool have = w.next(a, NR, true); have;) {
         const int row0 = w.g * NR, rows = min(NR, w.req.q * a.n_heads - row0);
         const int vis = w.vis;
+        // Tokens from here on are hidden from some of the group's rows (of earlier
+        // query tokens).  Their weights there are 0, and 0 x NaN is not: values that
+        // are not finite are made zero for the second product, and the output of the
+        // rows that do see them is made NaN in the end.
+        int hidden = INT32_MAX;
+        if (kMixed && w.req.q > 1) {
+            const int lo = seen(w.req, token_of(w.req, a.n_heads, row0));
+            hidden = lo < vis ? lo : INT32_MAX;
+        }
+        bool found = false;
         // how many keys this thread's rows see
         int lim[2];
 #pragma unroll
@@ -569,6 +633,15 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
                     if (active)
                         store_p();
                 }
+                if (kMixed && j0 + kTile > hidden) {
+                    // (the copies are waited for once more: these threads read them themselves)
+                    const int from = max(hidden - j0, 0), f = n % lay.fronts, b = n % lay.backs;
+                    const int got = clear_hidden(&sh.front_full[f], n / lay.fronts & 1, sm + lay.front + f * kFront * kChunk,
+                                                 &sh.back_full[b], n / lay.backs & 1, sm + lay.back + b * kBack * kChunk, from,
+                                                 8 * (min(vis - j0, kTile) - from), tid);
+                    found = found || got > 0;
+                    ok = __all_sync(0xffffffffu, ok && got >= 0);
+                }
                 if (j0 + kTile > vis) {
                     // rows of the tile that nobody sees may hold anything: their weights are 0, 0 x NaN is not
                     const int dead = kTile - (vis - j0);
@@ -646,7 +719,11 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
             if (active && t4 == 0 && half == 1)
                 sh.top[1][row_h[h]] = z[h];
         }
-        sync_some(1, kSoftThreads);
+        bool poisoned = false;
+        if constexpr (kMixed)
+            poisoned = sync_any(1, kSoftThreads, found);
+        else
+            sync_some(1, kSoftThreads);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = row_h[h];
@@ -709,6 +786,11 @@ __device__ __forceinline__ bool softmax_role(const w8_latent_paged &a, Walk w, u
         }
         fence_before(); // the loads of O, before the next run's products
         sync_some(1, kSoftThreads); // the rows' places and 1 / z are read
+        if (kMixed && poisoned) {
+            poison(a, w.r, row0, rows, max(hidden, w.off * kTile), int(min(int64_t(w.off + w.run) * kTile, int64_t(vis))), sh.out,
+                   whole ? nullptr : parts.o + size_t(slot) * kMaxRows * W8_LATENT_DIM, tid);
+            sync_some(1, kSoftThreads);
+        }
         w = nx;
         have = more;
     }
@@ -769,7 +851,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     int rows = 0, groups64 = 0;
     for (int r = r0; r < r1; ++r) {
         const Request q = r == r0 ? held : request_of(a, r);
-        rows = max(rows, min(q.q * a.n_heads, kMaxRows + 1));
+        rows = max(rows, min(q.q * a.n_heads, kMaxRows + 1) + (q.q > 1 ? kSeveral : 0));
         groups64 += groups_of(q, a.n_heads, 64);
     }
     // fewer rows a group: when no group would be filled, or when twice as many
@@ -787,6 +869,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         rows = max(rows, sh.max[i]);
         all64 += sh.few[i];
     }
+    // (those of a request of several query tokens are the most there are)
+    const bool several = rows >= kSeveral;
+    rows -= several ? kSeveral : 0;
     const int grid = int(gridDim.x), rows_max = rows;
     const int nr = rows > 32 && all64 * 2 > grid ? 64 : rows > 16 && all64 * 4 > grid ? 32 : 16;
     mine = nr != 64 ? tiles_of(nr, kBegin) : mine + int64_t(groups64) * kBegin;
@@ -852,7 +937,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                : role == kScoreWarp ? score_role<NR>(a, w, sm, sh, tm_s)
                : role == kOutWarp   ? out_role<NR>(a, w, sm, sh, tmem)
                : role == kQueryWarp ? query_role<NR>(a, w, sm, sh, lane)
-                                    : softmax_role<NR>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid);
+               : several && a.n_heads % NR ? softmax_role<NR, true>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid)
+                                           : softmax_role<NR, false>(a, w, sm, sh, tmem, tm_s, parts, total, ctas, tid);
     };
     const bool ok = nr == 64   ? roles(std::integral_constant<int, 64>{})
                     : nr == 32 ? roles(std::integral_constant<int, 32>{})

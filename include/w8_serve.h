@@ -145,9 +145,8 @@ w8_status w8_latent_cache_write(const uint16_t *latent, int64_t ld_latent, const
  * int32.  cu_q must not decrease; it is cut to 0 .. n_tok, seq_lens to
  * 0 .. max_pages * page_size.  Tokens that no request holds are not written.
  * Cached rows past a request's length are never used, whatever they hold; a
- * page number outside the cache reads as zeros.  A non-finite value in one
- * of the last n - 1 cached tokens of a request reaches every query token of
- * that request, the ones before it too.
+ * page number outside the cache reads as zeros.  A non-finite value in a
+ * cached token reaches the query tokens that see it, and no other.
  * scale: finite, > 0.  n_tok = 0 is a no-op.
  * workspace: w8_latent_paged_workspace_bytes bytes, 256-byte aligned; needs
  * no initialisation; calls that share one must not overlap on the GPU.
