@@ -104,15 +104,30 @@ __device__ __forceinline__ void softmax_half(uint32_t col, uint32_t o, int j0, i
     wait_st();
 }
 
+// s += 0 * (a, b): NaN where a value is not finite.
+__device__ __forceinline__ void add_times0(float2 &s, float a, float b)
+{
+    asm("{\n\t.reg .b64 v, t, z;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 t, {%0, %1};\n\tmov.b64 z, 0;\n\t"
+        "fma.rn.f32x2 t, v, z, t;\n\tmov.b64 {%0, %1}, t;\n\t}"
+        : "+f"(s.x), "+f"(s.y)
+        : "f"(a), "f"(b));
+}
+
 // 32 columns of O at `o`, times inv (zeros where there is no O), as bf16 into a
 // lane's row of `stage` (rows of `bytes` bytes), vectors v0 ..; swizzled, so that
-// neither these stores nor reads by rows conflict.
-__device__ __forceinline__ void stage32(uint8_t *stage, int bytes, uint32_t o, bool some, float inv, int v0, int lane)
+// neither these stores nor reads by rows conflict.  zero: 0, and NaN once a value is
+// not finite.
+__device__ __forceinline__ void stage32(uint8_t *stage, int bytes, uint32_t o, bool some, float inv, int v0, int lane, float &zero)
 {
     float v[32];
     if (some) {
         ld32x32(v, o);
         wait_ld();
+        float2 part[2] = {{zero, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            add_times0(part[i & 1], v[2 * i], v[2 * i + 1]);
+        zero = (part[0].x + part[0].y) + (part[1].x + part[1].y);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -124,6 +139,80 @@ __device__ __forceinline__ void stage32(uint8_t *stage, int bytes, uint32_t o, b
             u.w = pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv);
         }
         *reinterpret_cast<uint4 *>(stage + lane * bytes + (((v0 + i) ^ (lane & 7)) << 4)) = u;
+    }
+}
+
+__device__ __forceinline__ float2 widen2(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
+__device__ __forceinline__ const uint32_t *words(const uint16_t *p, int64_t tok, int64_t ld_tok, int head, int64_t ld_head)
+{
+    return reinterpret_cast<const uint32_t *>(p + tok * ld_tok + head * ld_head);
+}
+
+// Causality hides keys from some rows of a tile: their weights there are 0, but
+// 0 x NaN is not, nor 0 x infinity.  So rows whose output is not finite although
+// their sum of weights is, and which do not see all keys, are looked at again by a
+// warp: where a value among the keys below `end` that is hidden from a row is not
+// finite, the row's output is made once more from the keys it sees, one at a time.
+// (No input of finite values comes here, and none pays for it: values would have to
+// be searched before every diagonal tile's second product.)  bad: such rows of this
+// warp's 32, lane i's being query q0 + i with `lim` keys, reference m, sum z; the
+// warp's columns are d_v / 2 of them from DV / 2 * half on.
+template <int DN, int DV>
+__device__ __noinline__ void redo_rows(const w8_latent_expanded &a, uint32_t bad, int q0, int head, int k0, int end, int lim, float m,
+                                       float z, int half, int lane)
+{
+    constexpr int kQ = DN / 64, kV = DV / 128; // words of 2 values a lane
+    const float sl = a.scale * kLog2e;
+    // the last hidden key whose value is not finite in the warp's columns
+    int last = -1;
+    for (int j = __reduce_min_sync(0xffffffffu, bad >> lane & 1u ? lim : INT32_MAX); j < end; ++j) {
+        const uint32_t *v = words(a.v, k0 + j, a.ld_v_tok, head, a.ld_v_head) + DV / 4 * half + lane;
+        bool inf = false;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t u = __ldg(v + 32 * i);
+            inf = inf || (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u;
+        }
+        if (__any_sync(0xffffffffu, inf))
+            last = j;
+    }
+    bad &= __ballot_sync(0xffffffffu, lim <= last);
+    for (; bad; bad &= bad - 1) {
+        const int row = __ffs(int(bad)) - 1, keys = __shfl_sync(0xffffffffu, lim, row);
+        const float at = __shfl_sync(0xffffffffu, m, row), sum = __shfl_sync(0xffffffffu, z, row);
+        const float ref = at == -CUDART_INF_F ? 0.0f : at;
+        float2 q[kQ + 1], o[kV] = {};
+#pragma unroll
+        for (int i = 0; i < kQ; ++i)
+            q[i] = widen2(__ldg(words(a.q_nope, q0 + row, a.ld_qnope_tok, head, a.ld_qnope_head) + 32 * i + lane));
+        q[kQ] = widen2(__ldg(words(a.q_rope, q0 + row, a.ld_qrope_tok, head, a.ld_qrope_head) + lane));
+#pragma unroll 4
+        for (int j = 0; j < keys; ++j) {
+            const uint32_t *k = words(a.k_nope, k0 + j, a.ld_knope_tok, head, a.ld_knope_head) + lane;
+            const uint32_t *v = words(a.v, k0 + j, a.ld_v_tok, head, a.ld_v_head) + DV / 4 * half + lane;
+            float2 b = widen2(__ldg(words(a.k_rope, k0 + j, a.ld_krope_tok, 0, 0) + lane));
+            float x = fmaf(q[kQ].x, b.x, q[kQ].y * b.y);
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) {
+                b = widen2(__ldg(k + 32 * i));
+                x = fmaf(q[i].x, b.x, fmaf(q[i].y, b.y, x));
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+                x += __shfl_xor_sync(0xffffffffu, x, d);
+            const float p = ex2(fmaf(x, sl, -ref));
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                b = widen2(__ldg(v + 32 * i));
+                o[i].x = fmaf(p, b.x, o[i].x);
+                o[i].y = fmaf(p, b.y, o[i].y);
+            }
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        uint32_t *out = reinterpret_cast<uint32_t *>(a.out + (int64_t(q0) + row) * a.ld_out_tok + head * a.ld_out_head) + DV / 4 * half + lane;
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            out[32 * i] = pack_bf16(o[i].x * inv, o[i].y * inv);
     }
 }
 

@@ -320,9 +320,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         // made), so that a warp stores whole rows: a lane's row straight from
         // tensor memory took 32 half-used sectors a store, 4 us a CTA.
         uint8_t *const stage = sm + 32 * quarter * DV * 2; // of this pair of warps
+        float zero = 0.0f;
 #pragma unroll
         for (int c = 0; c < DV / 2; c += 32)
-            stage32(stage, DV * 2, tmem + lanes + uint32_t(DV / 2 * half + c), it.tiles > 0, inv, (DV / 2 * half + c) / 8, lane);
+            stage32(stage, DV * 2, tmem + lanes + uint32_t(DV / 2 * half + c), it.tiles > 0, inv, (DV / 2 * half + c) / 8, lane, zero);
         sync_some(1 + quarter, 64);
         constexpr int kVecs = DV / 8, kAtOnce = 32 / kVecs; // vectors of a row, rows of a store
 #pragma unroll 4
@@ -331,6 +332,12 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             if (i < it.rows)
                 *reinterpret_cast<uint4 *>(a.out + (int64_t(it.q0) + i) * a.ld_out_tok + head * a.ld_out_head + 8 * v) =
                     *reinterpret_cast<const uint4 *>(stage + mine * DV * 2 + ((v ^ (mine & 7)) << 4));
+        }
+        if (a.causal) {
+            const bool bad = zero != zero && z - z == 0.0f && row < it.rows && lim < it.nk;
+            if (sync_any(1 + quarter, 64, bad)) // the rows are stored
+                redo_rows<DN, DV>(a, __ballot_sync(0xffffffffu, bad), it.q0 + 32 * quarter, head, it.k0, min(it.tiles * kKeys, it.nk), lim,
+                                  m, z, half, lane);
         }
     }
     if (!ok)

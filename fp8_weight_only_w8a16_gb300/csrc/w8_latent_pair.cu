@@ -595,6 +595,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             }
             if (it.tiles <= 0)
                 look_ahead();
+            float zero = 0.0f;
             if (it.tiles >= 0) {
                 if (it.tiles > 0)
                     wait(&sh.o, n - 1);
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                         sync_some(1 + quarter, 64); // the columns before are stored
 #pragma unroll
                     for (int e = 0; e < 64; e += 32)
-                        stage32(stage, 256, o_at + uint32_t(c + 64 * half + e), it.tiles > 0, inv, 8 * half + e / 8, lane);
+                        stage32(stage, 256, o_at + uint32_t(c + 64 * half + e), it.tiles > 0, inv, 8 * half + e / 8, lane, zero);
                     if (c + 128 == DV && it.tiles > 0) { // O is read
                         fence_before();
                         __syncwarp();
@@ -640,6 +641,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             if (sync_any(1 + quarter, 64, !ok)) {
                 ok = false;
                 break;
+            }
+            if (a.causal) {
+                const uint32_t bad = __ballot_sync(0xffffffffu, zero != zero && z - z == 0.0f && row < it.rows && lim < it.nk);
+                if (bad)
+                    redo_rows<DN, DV>(a, bad, it.q0 + 32 * quarter, it.head, it.k0, min(it.tiles * kKeys, it.nk), lim, m, z, half, lane);
             }
             it = then;
         }

@@ -194,8 +194,7 @@ w8_status w8_latent_paged_workspace_bytes(int n_tok, int n_heads, int n_req, int
  * bf16, 16-byte aligned, strides multiples of 8; lse: device fp32
  * [n_q][n_heads], or NULL.  cu_q, cu_k [n_req + 1]: device int32, not
  * decreasing; cut to 0 .. n_q and 0 .. n_k.  Keys of other requests are never
- * used, whatever they hold; a non-finite value in a key that causality hides
- * from a query may still reach it when both lie in one tile.
+ * used, whatever they hold, nor are keys that causality hides from a query.
  * scale: finite, > 0.  n_q = 0 is a no-op; n_k may be 0.  One kernel launch. */
 typedef struct {
     const uint16_t *q_nope;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests.serve_util import attend64, lse_bound, out_bound
-from tests.test_gpu_serve_attention import Paged
+from tests.test_gpu_serve_attention import Expanded, Paged, pairs
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -81,3 +81,94 @@ def test_paged_all_later_tokens_bad(serve):
         assert torch.equal(out[t], want[t]) and torch.equal(lse[t], wl[t])
     for t in (1, 2, 3, 5, 6):
         assert torch.isnan(out[t]).all() and torch.isnan(lse[t]).all()
+
+
+# ---------------------------------------------------------------------------
+# expanded form
+# ---------------------------------------------------------------------------
+
+def check_head(out, lse, q, k, v, see, scale):
+    """One head's rows by the definition: a value that is not finite counts for the rows that see it alone, a
+    key that is not finite gives them a score of -inf (no weight) or a sum that is NaN."""
+    whole = torch.isfinite(k).all(1)
+    x = (q.double() @ k.double().T * scale).masked_fill(~see, float("-inf"))
+    lse64 = torch.logsumexp(torch.where(see, x, float("-inf")), 1)
+    nan = torch.isnan(x).any(1) | (x == float("inf")).any(1)
+    lse64 = torch.where(nan, float("nan"), lse64)
+    empty = torch.isneginf(lse64)
+    o, l, a, big = attend64(q, torch.where(whole[:, None], k, 0.0), torch.where(torch.isfinite(v), v, 0.0), scale,
+                            see & whole[None, :])
+    w = torch.exp(x - torch.where(empty, 0.0, lse64)[:, None])
+    for j in (~torch.isfinite(v).all(1)).nonzero()[:, 0].tolist():
+        o += torch.where(see[:, j, None], w[:, j, None] * torch.where(torch.isfinite(v[j]), 0.0, v[j].double()), 0.0)
+    o = torch.where(nan[:, None], float("nan"), o)
+    assert torch.equal(torch.isnan(lse), nan) and torch.equal(torch.isneginf(lse), empty)
+    ok = ~nan & ~empty
+    assert ((lse.double() - l).abs() <= lse_bound(l, big, q.shape[1], k.shape[0]))[ok].all()
+    fin = torch.isfinite(o)
+    assert torch.equal(torch.isnan(out), torch.isnan(o))
+    assert torch.equal(out[~fin & ~torch.isnan(o)].double(), o[~fin & ~torch.isnan(o)])
+    err, bound = (out.double() - o).abs(), out_bound(o, a, big, q.shape[1], k.shape[0])
+    assert (err <= bound)[fin].all(), float((err / bound)[fin].max())
+    return int((~fin).any(1).sum())
+
+
+EXPANDED = [([300, 65], [300, 80], 3), ([5, 129, 64], [5, 500, 64], 3), ([200, 7], [30, 0], 2),
+            ([1600], [1600], 64), ([520, 1111], [520, 1400], 64)]
+
+
+@pytest.mark.parametrize("nope,cols", [(192, 256), (128, 128)])
+@pytest.mark.parametrize("q,k,heads", EXPANDED)
+def test_expanded_later_keys_reach_no_earlier_query(serve, nope, cols, q, k, heads):
+    c = Expanded(q, k, heads, nope, cols, seed=sum(q), std=0.5)
+    assert pairs(serve, c) == (heads == 64)
+    clean, cl = c.run(serve)
+    g = torch.Generator().manual_seed(nope + heads)
+
+    def pick(n):
+        return int(torch.randint(0, n, (1,), generator=g))
+
+    reached = 0
+    for r, (n, keys) in enumerate(zip(q, k)):
+        if keys == 0:
+            continue
+        for what in ("v", "v", "v", "k_nope", "k_rope"):
+            # the request's last key, its first, any
+            j = c.cu_k[r] + [keys - 1, pick(keys), pick(keys), pick(keys)][pick(4)]
+            head = pick(heads)
+            x = getattr(c, what)
+            at = (j, pick(64)) if what == "k_rope" else (j, head, [0, x.shape[2] - 1, pick(x.shape[2])][pick(3)])
+            kept = x[at].clone()
+            x[at] = BAD[pick(3)]
+            out, lse = c.run(serve)
+            a, b, d, e = c.cu_q[r], c.cu_q[r + 1], c.cu_k[r], c.cu_k[r + 1]
+            see = torch.arange(keys, device="cuda")[None, :] <= keys - n + torch.arange(n, device="cuda")[:, None]
+            for h in range(heads):
+                if what == "k_rope" and h % 16 in (0, 15) or h == head:
+                    reached += check_head(out[a:b, h], lse[a:b, h], torch.cat([c.q_nope[a:b, h], c.q_rope[a:b, h]], 1),
+                                          torch.cat([c.k_nope[d:e, h], c.k_rope[d:e]], 1), c.v[d:e, h], see, c.scale)
+            others = [h for h in range(heads) if h != head] if what != "k_rope" else []
+            assert torch.equal(out[:, others], clean[:, others]) and torch.equal(lse[:, others], cl[:, others])
+            assert torch.equal(out[:a], clean[:a]) and torch.equal(out[b:], clean[b:])
+            x[at] = kept
+    assert reached > 0
+    out, lse = c.run(serve)
+    assert torch.equal(out, clean) and torch.equal(lse, cl)
+
+
+@pytest.mark.parametrize("nope,cols", [(192, 256), (128, 128)])
+@pytest.mark.parametrize("n,heads", [(300, 3), (1600, 64)])
+def test_expanded_all_later_keys_bad(serve, nope, cols, n, heads):
+    """Every key from one on holds nothing but NaN: the queries before it get what they get of the keys before it."""
+    c = Expanded([n], [n], heads, nope, cols, seed=n)
+    want, wl = c.run(serve)
+    at = n // 2 + 3
+    c.k_nope[at:], c.k_rope[at:], c.v[at:] = float("nan"), float("nan"), float("nan")
+    out, lse = c.run(serve)
+    assert torch.isnan(out[at:]).all() and torch.isnan(lse[at:]).all()
+    assert torch.equal(lse[:at], wl[:at]) and torch.isfinite(out[:at]).all()
+    for h in (0, heads - 1):
+        q = torch.cat([c.q_nope[:at, h], c.q_rope[:at, h]], 1)
+        k = torch.cat([c.k_nope[:at, h], c.k_rope[:at]], 1)
+        see = torch.ones(at, at, dtype=torch.bool, device="cuda").tril()
+        assert check_head(out[:at, h], lse[:at, h], q, k, c.v[:at, h], see, c.scale) == 0
