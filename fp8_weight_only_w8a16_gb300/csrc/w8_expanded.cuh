@@ -143,19 +143,27 @@ __device__ __forceinline__ void stage32(uint8_t *stage, int bytes, uint32_t o, b
 }
 
 __device__ __forceinline__ float2 widen2(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
-__device__ __forceinline__ const uint32_t *words(const uint16_t *p, int64_t tok, int64_t ld_tok, int head, int64_t ld_head)
-{
-    return reinterpret_cast<const uint32_t *>(p + tok * ld_tok + head * ld_head);
-}
+// Rows of an operand in words of two values, from a token and head on.
+struct Words {
+    const uint32_t *p;
+    int64_t ld;
+    __device__ __forceinline__ Words(const uint16_t *from, int64_t tok, int64_t ld_tok, int64_t column)
+        : p(reinterpret_cast<const uint32_t *>(from + tok * ld_tok + column)), ld(ld_tok / 2)
+    {
+    }
+    __device__ __forceinline__ uint32_t at(int tok, int i) const { return __ldg(p + tok * ld + i); }
+};
 
 // Causality hides keys from some rows of a tile: their weights there are 0, but
 // 0 x NaN is not, nor 0 x infinity.  So rows whose output is not finite although
 // their sum of weights is, and which do not see all keys, are looked at again by a
 // warp: where a value among the keys below `end` that is hidden from a row is not
 // finite, the row's output is made once more from the keys it sees, one at a time.
-// (No input of finite values comes here, and none pays for it: values would have to
-// be searched before every diagonal tile's second product.)  bad: such rows of this
-// warp's 32, lane i's being query q0 + i with `lim` keys, reference m, sum z; the
+// (No input of finite values comes here: searching the values before every diagonal
+// tile's second product would hold that up.  A prompt of 4096 at 64 heads: 386 us, one
+// value that all see NaN 600, half of all 956, all of them 1350.  A key of a row takes
+// 0.1 us; the other warps wait up to 5 s, or 1.6 million keys for 32 rows.)  bad: such
+// rows of this warp's 32, lane i's being query q0 + i with `lim` keys, reference m, sum z; the
 // warp's columns are d_v / 2 of them from DV / 2 * half on.
 template <int DN, int DV>
 __device__ __noinline__ void redo_rows(const w8_latent_expanded &a, uint32_t bad, int q0, int head, int k0, int end, int lim, float m,
@@ -163,14 +171,19 @@ __device__ __noinline__ void redo_rows(const w8_latent_expanded &a, uint32_t bad
 {
     constexpr int kQ = DN / 64, kV = DV / 128; // words of 2 values a lane
     const float sl = a.scale * kLog2e;
+    const Words qn(a.q_nope, q0, a.ld_qnope_tok, head * a.ld_qnope_head + 2 * lane),
+        qr(a.q_rope, q0, a.ld_qrope_tok, head * a.ld_qrope_head + 2 * lane),
+        kn(a.k_nope, k0, a.ld_knope_tok, head * a.ld_knope_head + 2 * lane), kr(a.k_rope, k0, a.ld_krope_tok, 2 * lane),
+        v(a.v, k0, a.ld_v_tok, head * a.ld_v_head + DV / 2 * half + 2 * lane);
+    uint16_t *const out = a.out + int64_t(q0) * a.ld_out_tok + head * a.ld_out_head + DV / 2 * half + 2 * lane;
+    const int64_t ld_out = a.ld_out_tok;
     // the last hidden key whose value is not finite in the warp's columns
     int last = -1;
     for (int j = __reduce_min_sync(0xffffffffu, bad >> lane & 1u ? lim : INT32_MAX); j < end; ++j) {
-        const uint32_t *v = words(a.v, k0 + j, a.ld_v_tok, head, a.ld_v_head) + DV / 4 * half + lane;
         bool inf = false;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t u = __ldg(v + 32 * i);
+            const uint32_t u = v.at(j, 32 * i);
             inf = inf || (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u;
         }
         if (__any_sync(0xffffffffu, inf))
@@ -184,35 +197,49 @@ __device__ __noinline__ void redo_rows(const w8_latent_expanded &a, uint32_t bad
         float2 q[kQ + 1], o[kV] = {};
 #pragma unroll
         for (int i = 0; i < kQ; ++i)
-            q[i] = widen2(__ldg(words(a.q_nope, q0 + row, a.ld_qnope_tok, head, a.ld_qnope_head) + 32 * i + lane));
-        q[kQ] = widen2(__ldg(words(a.q_rope, q0 + row, a.ld_qrope_tok, head, a.ld_qrope_head) + lane));
-#pragma unroll 4
-        for (int j = 0; j < keys; ++j) {
-            const uint32_t *k = words(a.k_nope, k0 + j, a.ld_knope_tok, head, a.ld_knope_head) + lane;
-            const uint32_t *v = words(a.v, k0 + j, a.ld_v_tok, head, a.ld_v_head) + DV / 4 * half + lane;
-            float2 b = widen2(__ldg(words(a.k_rope, k0 + j, a.ld_krope_tok, 0, 0) + lane));
-            float x = fmaf(q[kQ].x, b.x, q[kQ].y * b.y);
+            q[i] = widen2(qn.at(row, 32 * i));
+        q[kQ] = widen2(qr.at(row, 0));
+        // from the last key back, some at a time, until all is NaN: a row that sees such
+        // values mostly does so near its end
+        constexpr int kAtOnce = 8;
+        bool left = true;
+        for (int j1 = keys; j1 > 0 && left; j1 -= kAtOnce) {
+            float p[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kQ; ++i) {
-                b = widen2(__ldg(k + 32 * i));
-                x = fmaf(q[i].x, b.x, fmaf(q[i].y, b.y, x));
+            for (int n = 0; n < kAtOnce; ++n) {
+                const int j = max(j1 - 1 - n, 0);
+                float2 b = widen2(kr.at(j, 0));
+                p[n] = fmaf(q[kQ].x, b.x, q[kQ].y * b.y);
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    b = widen2(kn.at(j, 32 * i));
+                    p[n] = fmaf(q[i].x, b.x, fmaf(q[i].y, b.y, p[n]));
+                }
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1)
-                x += __shfl_xor_sync(0xffffffffu, x, d);
-            const float p = ex2(fmaf(x, sl, -ref));
+#pragma unroll
+                for (int n = 0; n < kAtOnce; ++n)
+                    p[n] += __shfl_xor_sync(0xffffffffu, p[n], d);
+            bool nan = true;
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                b = widen2(__ldg(v + 32 * i));
-                o[i].x = fmaf(p, b.x, o[i].x);
-                o[i].y = fmaf(p, b.y, o[i].y);
+#pragma unroll
+                for (int n = 0; n < kAtOnce; ++n)
+                    if (n < j1) {
+                        const float2 b = widen2(v.at(j1 - 1 - n, 32 * i));
+                        const float w = ex2(fmaf(p[n], sl, -ref));
+                        o[i].x = fmaf(w, b.x, o[i].x);
+                        o[i].y = fmaf(w, b.y, o[i].y);
+                    }
+                nan = nan && o[i].x != o[i].x && o[i].y != o[i].y;
             }
+            left = !__all_sync(0xffffffffu, nan);
         }
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        uint32_t *out = reinterpret_cast<uint32_t *>(a.out + (int64_t(q0) + row) * a.ld_out_tok + head * a.ld_out_head) + DV / 4 * half + lane;
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-            out[32 * i] = pack_bf16(o[i].x * inv, o[i].y * inv);
+            *reinterpret_cast<uint32_t *>(out + row * ld_out + 64 * i) = pack_bf16(o[i].x * inv, o[i].y * inv);
     }
 }
 

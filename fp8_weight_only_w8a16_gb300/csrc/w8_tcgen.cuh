@@ -33,7 +33,7 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
                  : "memory");
 }
-// Wait for the phase of the given parity; false after kPolls polls.
+// Wait for the phase of the given parity; false after kPolls polls (of 1.3 us: 5 s).
 constexpr uint32_t kPolls = 1u << 22;
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
 {
