@@ -108,6 +108,32 @@ def test_paged_long_contexts_are_split(serve, lens, heads):
     Paged(lens, [1] * len(lens), heads, 64, seed=len(lens)).check(serve)
 
 
+@pytest.mark.parametrize("lens,q_lens", [
+    ([40000], [1]), ([20011, 7], [1, 1]), ([9000, 1, 12000], [1, 1, 1]), ([64 * 152 + 1], [1]), ([30011, 640], [2, 3]),
+    ([1 + 997 * i % 5000 for i in range(150)], [1] * 150)])
+@pytest.mark.parametrize("heads", [16, 20, 64])
+def test_paged_every_token_counts_once(serve, lens, q_lens, heads):
+    """Queries of zeros weigh every token alike, and a token's value says which tile it lies in: the weights
+    (1), their sums (whole numbers below 2^24) and so O and z are exact.  Left are the logarithm and its
+    product, 2^-21 + 2^-22 of the log-sum, and the quotient's rounding to bf16, 2^-8 of it: a token that is
+    lost or taken twice is 1 / 40000 of z, a tile the whole of its column."""
+    c = Paged(lens, q_lens, heads, 64, seed=len(lens))
+    c.q_lat, c.q_rope = torch.zeros_like(c.q_lat), torch.zeros_like(c.q_rope)
+    for r, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        rows = torch.zeros(n, 576, dtype=BF, device="cuda")
+        rows[j, j // 64 % 512] = 1
+        c.cache[c.table[r, j // 64].long(), j % 64] = rows
+    out, lse = c.run(serve)
+    for r, (n, q) in enumerate(zip(lens, q_lens)):
+        for i in range(q):
+            t, m = c.cu[r] + i, n - q + i + 1
+            want = torch.log(torch.tensor(float(m), dtype=torch.float64))
+            assert (lse[t].double().cpu() - want).abs().max() <= 2.0 ** -21 + 2.0 ** -22 * want
+            share = torch.bincount(torch.arange(m, device="cuda") // 64 % 512, minlength=512).double() / m
+            assert ((out[t].double() - share).abs() <= 2.0 ** -8 * (1 + 2.0 ** -7) * share).all()
+
+
 def test_paged_many_requests(serve):
     g = torch.Generator().manual_seed(1)
     lens = torch.randint(0, 200, (700,), generator=g).tolist()

@@ -81,6 +81,29 @@ def test_more_rows_than_counters(serve):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab,top,ld,offset", [
+    (1, 154880, 0, None, 0), (1, 154880, 5, None, 3), (48, 129283, 0, 129290, 1), (3, 32003, 20, None, 7), (700, 4097, 1, None, 1),
+    (5, 9, 0, 11, 2), (2, 154880, 0, None, 1)])
+def test_every_logit_counts_once(serve, dtype, rows, vocab, top, ld, offset):
+    """Equal logits: the terms are 1 and their sum a whole number below 2^24, both exact, so that only the
+    logarithm's rounding is left (2 units): a vector that is lost or taken twice is 4 / 154880 of the sum at
+    least.  Then larger logits in the row's first and last places, where vectors stick out of it: their terms
+    add 2^-20 of the sum."""
+    x, _ = logits(rows, vocab, dtype, 1, ld, offset)
+    tok = torch.arange(rows, device="cuda").to(torch.int32) % vocab
+    x.fill_(2.5)
+    lp, ent, _, _ = run(serve, x, tok, top)
+    want = torch.log(torch.tensor(float(vocab), dtype=torch.float64, device="cuda"))
+    bound = 2 * U * 16 + 4 * U * 2.5
+    assert ((lp.double() + want).abs() <= bound).all() and ((ent.double() - want).abs() <= bound).all()
+    x[:, :7], x[:, -7:] = 5.0, 5.5
+    lp, ent, _, _ = run(serve, x, tok, top)
+    wlp, went, _, _, _ = logprobs64(x, tok, top)
+    assert ((lp.double() - wlp).abs() <= bound + 2.0 ** -20).all()
+    assert ((ent.double() - went).abs() <= bound + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("order", ["ascending", "descending", "equal", "pairs"])
 def test_order_of_the_logits(serve, dtype, order):
     """Every logit beats the ones before it; or all are equal (the lowest token first)."""
