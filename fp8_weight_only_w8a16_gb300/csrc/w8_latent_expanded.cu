@@ -20,7 +20,7 @@
 // shared memory.
 //
 // Measured (replayed): three prompts of 37 to 611 tokens at 16 heads of 128 + 64
-// / 128 in 11.8 us, bound by the chain scores - softmax - output of a tile; a
+// / 128 in 11.9 us, bound by the chain scores - softmax - output of a tile; a
 // full tile of 192 + 64 / 256 takes 2566 cycles, 2048 of them steps, and wants
 // 50 bytes a cycle and SM from L2.
 #include "w8_copies.h"
@@ -376,9 +376,10 @@ cudaError_t launch_latent_expanded(const w8_latent_expanded &a, int sms, cudaStr
     // Pairs of CTAs halve what comes from L2 and run on from item to item, but
     // start later and pad queries to 256: they pay from about five waves of
     // 128-query tiles on, of requests that fill their tiles.  64 heads of
-    // 192 + 64 / 256, one prompt of 4096: 365 us in pairs, 391 by CTAs; of 2048:
-    // 121 and 127; of 1024: 50.0 and 49.5; 32 requests of 20: 132 and 109; 16
-    // heads, 9 requests of 700: 64 and 69; one of 1024: 25 and 16.
+    // 192 + 64 / 256, one prompt of 4096: 367 us in pairs, 387 by CTAs; of 2048:
+    // 123 and 128; of 1024: 50.9 and 50.4; 32 requests of 20: 136 and 113; 16
+    // heads, 9 requests of 700: 65 and 70; one of 1024: 26 and 16.  (64 heads of
+    // 128 + 64 / 128, one prompt of 4096: 304 and 296.)
     if (int64_t(a.n_q) * a.n_heads >= int64_t(5) * kRows * sms && a.n_q / a.n_req >= 512)
         return launch_expanded_pairs(a, s);
     return a.d_nope == 192 ? launch<192, 256>(a, s) : launch<128, 128>(a, s);

@@ -48,12 +48,12 @@
 // the line's length picks NR: 64 rows a group, or fewer when there are not
 // enough tiles to give every SM one.
 //
-// Measured (replayed, 64 heads): 128 requests of up to 16384 tokens 200 us,
-// 5.9 TB/s of HBM in the first kernel, about the rate of a copy; 24 requests of
-// 1 to 4 query tokens over up to 8111 tokens 72 us, bound by the chain copy -
-// scores - softmax - output with two tiles in flight (2900 cycles a tile, the
-// tensor cores' share 1920) and by the parts (26 MB written and read back); one
-// request of 1531 tokens 13 us, latency.
+// Measured (replayed, 64 heads): 128 requests of up to 16384 tokens, 0.99 million
+// in all, 197 to 200 us for 1.16 GB (170 us at the rate of a copy), 6.1 TB/s in the
+// first kernel, 1.10 million 221 us (190); 24 requests of 1 to 4 query tokens over up
+// to 8111 tokens 66 to 73 us, bound by the chain copy - scores - softmax - output with
+// two tiles in flight (2900 cycles a tile, the tensor cores' share 1920) and by the
+// parts (26 MB written and read back); one request of 1531 tokens 13 us, latency.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>

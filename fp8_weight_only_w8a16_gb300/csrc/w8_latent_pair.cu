@@ -27,8 +27,8 @@
 // off the grid by cancelling a launch (clusterlaunchcontrol), so that the next
 // item's copies and first scores run while this one's output is stored.
 //
-// Measured (replayed): a prompt of 4096 at 64 heads of 192 + 64 / 256 in 365 to
-// 374 us, 1.5 PFLOP/s, tensor pipe 65 %.  A tile takes 2310 cycles of which 2048
+// Measured (replayed): a prompt of 4096 at 64 heads of 192 + 64 / 256 in 366 to
+// 384 us by the clock, 1.5 PFLOP/s at best, tensor pipe 64 %.  A tile takes 2310 cycles of which 2048
 // are steps: the scores of tile i + 2 wait for the output of tile i, whose
 // weights lie in the same columns, and nothing else is left to run meanwhile.
 // The rest is the 3400 cycles of an item's output, of which the next one's

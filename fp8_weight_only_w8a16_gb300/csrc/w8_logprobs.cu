@@ -20,10 +20,10 @@
 // place is the number of larger keys gathered.  The loop over the logits knows
 // nothing of the selection.
 //
-// Measured (replayed, 154880 logits): 1024 bf16 rows with 1 alternative 59 us,
-// 5.4 TB/s (without alternatives 52, fp32 95 us = 6.7 TB/s: HBM); 48 fp32 rows
+// Measured (replayed, 154880 logits): 1024 bf16 rows with 1 alternative 59 to 61
+// us, 5.3 TB/s (without alternatives 53, fp32 94 us = 6.7 TB/s: HBM); 48 fp32 rows
 // with 20 alternatives 15 us, one bf16 row with 5 alternatives 8.7 us, without
-// 4.7: the selection and the join are chains of a few us that only many rows
+// 4.3: the selection and the join are chains of a few us that only many rows
 // hide.  bf16 is at 62 % of the issue slots, six instructions a logit.
 //
 // A row is cut into `splits` runs of whole 16-byte vectors, one a CTA; the
