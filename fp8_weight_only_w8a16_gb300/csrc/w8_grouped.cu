@@ -298,15 +298,19 @@ __device__ __forceinline__ Item find(const Shared &sh, int groups, int blocks, i
     return it;
 }
 
-// g / (1 + e^-g) u.  e^-g = 2^t, t = -g log2 e rounded: off by 0.69 |t| 2^-24
-// of its value, 2^-17.6 at most before it is past every finite value; ex2, the
-// reciprocal and the products add 6 units: within 2^-17 in all, and 0 where the
-// reciprocal of 1 + e^-g is below 2^-126.
+// g / (1 + e^-g) u.  With h = e^(-|g| / 2), 1 + e^-|g| = 1 + h h lies in 1 .. 2, and
+// for g < 0 the fraction's e^g is split between both factors: nothing overflows, and
+// a gate far below 0 leaves what the definition gives as long as bf16 holds it
+// (silu(-100) u for a large u, too).  CUDA's expf is within 2 units (2^-22), counted
+// twice in h h and in the factors, at most half as much in 1 + h h; the reciprocal is
+// within one, the sum and the four products within half a unit each: in all
+// (2 + 1 + 0.5 + 5 / 4) 2^-22 < 2^-19.7 of the value.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
+    const float h = expf(-0.5f * fabsf(g)), f = g < 0.0f ? h : 1.0f;
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(g * -1.4426950408889634f)));
-    return g * r * u;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.0f)));
+    return g * r * f * (u * f);
 }
 
 template <bool kFp8, bool kSilu, int kSize>

@@ -111,7 +111,8 @@ w8_status w8_group_rows_workspace_bytes(int n, int n_groups, size_t *bytes);
  *   y[y_rows[i]][j] = bf16( silu(g_j) u_j ),  silu(v) = v / (1 + exp(-v)),
  * g_j and u_j the scaled fp32 sums of source rows j and I + j.  Sums are fp32;
  * the one rounding is the output's (w8_gemv_silu_mul rounds g and u to bf16
- * first, as two steps would; here nothing reads them).  Without silu_mul a
+ * first, as two steps would; here nothing reads them); silu(g) u is made within
+ * 2^-19 of its value, for gates far below 0, too.  Without silu_mul a
  * gate_up plane's outputs are in source row order.
  * x: device bf16 [n_x][ldx], 16-byte aligned, ldx >= K and a multiple of 8;
  * y: device bf16 [n_y][ldy], 2-byte aligned; x_rows, y_rows: device int32
