@@ -42,6 +42,7 @@
 
 #include "w8_grouped_internal.h"
 #include "w8_internal.h"
+#include "w8_sum_parts.h"
 #include "w8_tcgen.cuh"
 
 namespace w8 {
@@ -113,23 +114,6 @@ struct Turn {
             k = 0;
             parity ^= 1u;
         }
-    }
-};
-// Which parts of the sums an item has, and how often each has been used: the
-// issuer and the warps that store count alike.
-struct Parts {
-    uint32_t used = 0, parity = 0; // a bit a part: whether it has been used, whether an odd number of times
-    uint32_t mask = 0, next = 1;   // the item's parts, the next small item's
-    __device__ __forceinline__ void take(int n, int cols)
-    {
-        mask = n > cols ? 3u : next;
-        next = n > cols ? next : next ^ 3u;
-    }
-    __device__ __forceinline__ uint32_t first() const { return mask == 2 ? 1u : 0u; }
-    __device__ __forceinline__ void done()
-    {
-        used |= mask;
-        parity ^= mask;
     }
 };
 // Waits for the last use of every slot.
@@ -551,8 +535,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                     const uint32_t idesc = inst_desc(256, size, false, false);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (parts.mask & parts.used & (1u << i)) // its last use: of the other parity than the next
-                            ok = ok && bar_wait(&sh.sums_read[i], (parts.parity >> i & 1u) ^ 1u);
+                        if (parts.frees(i))
+                            ok = ok && bar_wait(&sh.sums_read[i], parts.free_parity(i));
                     const uint32_t sums = parts.first() * kPart;
                     bool there = false; // the stage was seen to be ready while the one before was issued
                     for (int st = 0; st < stages && ok; ++st) {
@@ -581,7 +565,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (ok && (parts.mask >> i & 1u))
+                        if (ok && parts.fills(i))
                             pair_commit(&sh.sums[i]);
                 };
                 uint32_t who;
@@ -715,7 +699,10 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                     }
                 }
             };
-            ok = warp_wait(&sh.sums[parts.first()], parts.parity >> parts.first() & 1u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (parts.fills(i))
+                    ok = ok && warp_wait(&sh.sums[i], parts.fill_parity(i));
             if (!ok)
                 break;
             fence_after();
@@ -738,7 +725,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                     if (lane == 0)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            if (parts.mask >> i & 1u)
+                            if (parts.fills(i))
                                 pair_arrive(read_bar + uint32_t(8 * i));
                 }
                 if (!some)
