@@ -188,12 +188,11 @@ __global__ void __launch_bounds__(kGrThreads) place_kernel(const GroupArgs a)
 
 cudaError_t launch_group_rows(const GroupArgs &a, cudaStream_t s)
 {
-    static std::atomic<uint64_t> done_count, done_place;
+    static std::atomic<uint64_t> raised{0};
     const size_t smem = size_t(kGrWarps) * size_t(a.groups) * sizeof(int);
     constexpr int most = kGrWarps * W8_MAX_GROUPS * int(sizeof(int));
-    cudaError_t e = raise_smem(done_place, reinterpret_cast<const void *>(&place_kernel), most);
-    if (e == cudaSuccess)
-        e = raise_smem(done_count, reinterpret_cast<const void *>(&count_kernel), most);
+    cudaError_t e = raise_smem(raised, {{reinterpret_cast<const void *>(&place_kernel), most},
+                                        {reinterpret_cast<const void *>(&count_kernel), most}});
     if (e != cudaSuccess)
         return e;
     if (a.chunks > 1) {

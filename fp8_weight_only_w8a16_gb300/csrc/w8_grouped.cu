@@ -39,6 +39,7 @@
 #include <stddef.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "w8_grouped_internal.h"
 #include "w8_internal.h"
@@ -797,10 +798,6 @@ template <bool kFp8, bool kSilu, int kSize>
 cudaError_t launch(const GroupedArgs &a, int sms, cudaStream_t s)
 {
     auto *fn = &grouped_kernel<kFp8, kSilu, kSize>;
-    static std::atomic<uint64_t> raised{0};
-    const cudaError_t e = raise_smem(raised, reinterpret_cast<const void *>(fn), kSmem);
-    if (e != cudaSuccess)
-        return e;
     constexpr Stages cfg = kStagesOf[kFp8][kSize];
     CUtensorMap map, map_w;
     if (!encode_weight_map(&map_w, a, run_bytes(kFp8)))
@@ -852,10 +849,20 @@ cudaError_t launch_sized(const GroupedArgs &a, int sms, cudaStream_t s)
                                       : launch<kFp8, kSilu, 2>(a, sms, s);
 }
 
+// Every kernel's limit, at the first call on a device.
+template <int... kI> cudaError_t raise_all(std::integer_sequence<int, kI...>)
+{
+    static std::atomic<uint64_t> raised{0};
+    return raise_smem(raised, {{reinterpret_cast<const void *>(&grouped_kernel<kI / 6 != 0, kI / 3 % 2 != 0, kI % 3>), kSmem}...});
+}
+
 } // namespace
 
 cudaError_t launch_grouped(const GroupedArgs &a, bool fp8, int sms, cudaStream_t s)
 {
+    const cudaError_t e = raise_all(std::make_integer_sequence<int, 12>{});
+    if (e != cudaSuccess)
+        return e;
     if (a.act == kActSiluMul)
         return fp8 ? launch_sized<true, true>(a, sms, s) : launch_sized<false, true>(a, sms, s);
     return fp8 ? launch_sized<true, false>(a, sms, s) : launch_sized<false, false>(a, sms, s);

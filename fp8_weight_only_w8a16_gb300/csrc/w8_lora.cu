@@ -817,31 +817,34 @@ int most_tiles(int n_rows, int n_adapters, int rows)
     return n_rows / rows + (n_adapters < n_rows ? n_adapters : n_rows);
 }
 
+constexpr int shrink_smem(int tiles) { return kLoWarps * tiles * 256 * int(sizeof(float)); }
+static_assert(shrink_smem(4) <= 48 * 1024, "no raised limit below eight tiles");
+
+// Every kernel's limit, at the first call on a device.
+cudaError_t raise_all()
+{
+    static std::atomic<uint64_t> raised{0};
+    return raise_smem(raised, {{reinterpret_cast<const void *>(&shrink_kernel<8>), shrink_smem(8)},
+                               {reinterpret_cast<const void *>(&shrink_tc_kernel<64>), ShrinkTc<64>::kSmem},
+                               {reinterpret_cast<const void *>(&shrink_tc_kernel<128>), ShrinkTc<128>::kSmem},
+                               {reinterpret_cast<const void *>(&expand_tc_kernel<64>), LoraTc<64>::kSmem},
+                               {reinterpret_cast<const void *>(&expand_tc_kernel<128>), LoraTc<128>::kSmem}});
+}
+
 int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
 template <int kTiles>
 cudaError_t shrink(const w8_lora &a, float *v, int splits, cudaStream_t s)
 {
-    constexpr int smem = kLoWarps * kTiles * 256 * int(sizeof(float));
-    if (smem > 48 * 1024) {
-        static std::atomic<uint64_t> done;
-        const cudaError_t e = raise_smem(done, reinterpret_cast<const void *>(&shrink_kernel<kTiles>), smem);
-        if (e != cudaSuccess)
-            return e;
-    }
     return launch_dependent(shrink_kernel<kTiles>,
-                            dim3(unsigned(most_tiles(a.n_rows, a.n_adapters, kShrinkRows)), unsigned(splits)), kLoThreads, smem, s, a,
-                            v, splits);
+                            dim3(unsigned(most_tiles(a.n_rows, a.n_adapters, kShrinkRows)), unsigned(splits)), kLoThreads,
+                            size_t(shrink_smem(kTiles)), s, a, v, splits);
 }
 
 template <int kRank>
 cudaError_t shrink_tc(const w8_lora &a, float *v, int rank16, int sms, cudaStream_t s)
 {
     using L = ShrinkTc<kRank>;
-    static std::atomic<uint64_t> done;
-    const cudaError_t e = raise_smem(done, reinterpret_cast<const void *>(&shrink_tc_kernel<kRank>), L::kSmem);
-    if (e != cudaSuccess)
-        return e;
     CUtensorMap map;
     const uint64_t sizes[3] = {uint64_t(a.k), uint64_t(a.rank), uint64_t(a.n_adapters)};
     const uint64_t strides[2] = {uint64_t(a.ld_a_row) * 2, uint64_t(a.n_adapters > 1 ? a.ld_a : a.rank * a.ld_a_row) * 2};
@@ -856,10 +859,6 @@ template <int kRank>
 cudaError_t expand_tc(const w8_lora &a, const float *v, int rank16, int sms, int ranges, cudaStream_t s)
 {
     using L = LoraTc<kRank>;
-    static std::atomic<uint64_t> done;
-    const cudaError_t e = raise_smem(done, reinterpret_cast<const void *>(&expand_tc_kernel<kRank>), L::kSmem);
-    if (e != cudaSuccess)
-        return e;
     CUtensorMap map;
     const uint64_t sizes[3] = {uint64_t(a.rank), uint64_t(a.n), uint64_t(a.n_adapters)};
     const uint64_t strides[2] = {uint64_t(a.ld_b_row) * 2, uint64_t(a.n_adapters > 1 ? a.ld_b : a.n * a.ld_b_row) * 2};
@@ -946,6 +945,9 @@ cudaError_t lora_status(int *out, bool reset)
 
 cudaError_t launch_lora(const w8_lora &a, float *v, int sms, cudaStream_t s)
 {
+    const cudaError_t e = raise_all();
+    if (e != cudaSuccess)
+        return e;
     switch (rank_tiles(a.rank)) {
     case 1: return lora<1>(a, v, sms, s);
     case 2: return lora<2>(a, v, sms, s);

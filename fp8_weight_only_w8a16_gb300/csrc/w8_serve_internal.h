@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "w8_serve.h"
 
@@ -76,6 +77,28 @@ inline cudaError_t raise_smem(std::atomic<uint64_t> &done, const void *fn, int b
     if (e == cudaSuccess && dev < 64)
         done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     return e;
+}
+
+// ... of all kernels of an operator, whichever of them the call goes to: a capture
+// that comes after one call of the operator sets no attribute.
+struct SmemLimit {
+    const void *fn;
+    int bytes;
+};
+inline cudaError_t raise_smem(std::atomic<uint64_t> &done, std::initializer_list<SmemLimit> kernels)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)))
+        return e;
+    for (const SmemLimit &k : kernels) {
+        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.bytes);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (dev < 64)
+        done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return cudaSuccess;
 }
 
 // Launch with the programmatic-dependency attribute (the kernel waits for the

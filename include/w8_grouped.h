@@ -17,8 +17,9 @@
  * to the current device, the caller owns every buffer, every function returns
  * a w8_status, arguments are checked on the host before anything is enqueued,
  * every call is asynchronous on the caller's stream and may be captured in a
- * CUDA graph (the first call of an operator on a device must come before a
- * capture: it raises the kernels' shared-memory limits).  Kernels are launched
+ * CUDA graph (the first call of an operator on a device, of any size and type,
+ * must come before a capture: it raises the shared-memory limits of all of the
+ * operator's kernels).  Kernels are launched
  * with programmatic dependent launch and read no caller's buffer before the
  * previous kernel of the stream has completed.  No output may lie on an input,
  * but for out on y (or add), row on row, where a function says so.
