@@ -480,4 +480,12 @@ inline Plan make_plan(int64_t n, int64_t k, int m, int sm_count)
     return use_tc(n, m) ? make_tc_plan(n, k, m, sm_count) : make_ring_plan(n, k, m, sm_count);
 }
 
+// Steps of columns that a CTA of the adapters' second product takes: what makes one
+// wave of four CTAs an SM of `tiles` tiles of `blocks` steps, 8 at most.
+inline int expand_steps(int64_t tiles, int64_t blocks, int sms)
+{
+    const int64_t per = ceil_div(tiles * blocks, 4 * int64_t(sms));
+    return per < 1 ? 1 : per < 8 ? int(per) : 8;
+}
+
 } // namespace w8

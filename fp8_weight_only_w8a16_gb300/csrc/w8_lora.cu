@@ -901,8 +901,7 @@ cudaError_t lora(const w8_lora &a, float *v, int sms, cudaStream_t s)
     const int tiles = most_tiles(a.n_rows, a.n_adapters, 16);
     constexpr int kStep = 32 * kLoWarps;
     int blocks = (a.n + kStep - 1) / kStep;
-    int per = int((int64_t(tiles) * blocks + 4 * sms - 1) / (4 * sms)); // steps a CTA: one wave of four CTAs an SM
-    per = per < 8 ? per : 8;
+    const int per = expand_steps(tiles, blocks, sms);
     blocks = (blocks + per - 1) / per;
     const dim3 grid{unsigned(tiles), unsigned(blocks)};
     return fast ? launch_dependent(expand_kernel<kTiles, true>, grid, kLoThreads, 0, s, a, v, splits, per * kStep)
