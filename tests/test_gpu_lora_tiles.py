@@ -121,3 +121,26 @@ def test_many_times_the_same_bits(grouped, rank, k):
     c.compare(first, offsets)
     for _ in range(25):
         assert torch.equal(c.run(offsets), first)
+
+
+@pytest.mark.parametrize("rank,k,toks", [(64, 4096, 600), (64, 512, 600), (128, 520, 600), (64, 512, 40), (16, 512, 600)])
+def test_weights_that_are_not_finite_stay_in_their_places(grouped, rank, k, toks):
+    """A NaN or an infinity in a row of B reaches that column of its adapter's rows, one in A all of the adapter's columns."""
+    c = Call(grouped, rank, k, toks=toks)
+    offsets = groups_of([toks // 2, 0, toks // 4, toks - toks // 2 - toks // 4])
+    clean = c.run(offsets)
+    c.compare(clean, offsets)
+    mine = c.order[toks // 2:toks // 2 + toks // 4].long()
+    others = torch.ones(toks, dtype=torch.bool, device="cuda")
+    others[mine] = False
+    columns = torch.ones(264, dtype=torch.bool, device="cuda")
+    columns[[17, 263]] = False
+    old = c.b[2, [17, 263], 3].clone()
+    c.b[2, 17, 3], c.b[2, 263, 3] = INF, NAN
+    out = c.run(offsets)
+    assert torch.equal(out[others], clean[others]) and torch.equal(out[mine][:, columns], clean[mine][:, columns])
+    assert not torch.isfinite(out[mine][:, ~columns]).any()
+    c.b[2, [17, 263], 3] = old
+    c.a[2, 5, k - 1] = NAN
+    out = c.run(offsets)
+    assert torch.equal(out[others], clean[others]) and torch.isnan(out[mine]).all()
