@@ -25,14 +25,23 @@
 //
 // Bound: few rows a group, the planes' bytes; many, the tensor cores' rate (or the
 // power limit).  64 planes of 4096 x 6144 E4M3 (1.6 GB):
-//   2 rows each, SiLU    258 us  6.3 TB/s of HBM, tensor cores 16 % of the time
-//   128 rows each, SiLU  361 us  1.14 PFLOP/s: an item's 48 stages of 128 columns
-//                                wait for the widening (447 cycles a CTA and stage)
-//   512 rows each        885 us  1.86 PFLOP/s, the measured rate of the tensor cores
-// and 64 of 6144 x 2048 with 256 rows each 296 us, 1.39 PFLOP/s: items of 16 stages
-// pay for their begin and end.  Few planes (8 of 4096 x 6144 make 128 items, two
-// rounds of the 76 pairs) are bound by what one pair takes in, a stage of 256
-// columns in 1240 cycles: 42 us where their bytes take 30.
+//   2 rows each, SiLU    255 us  6.3 TB/s of HBM (bf16 planes 7.2), tensor cores 16 %
+//                                of the time
+//   128 rows each, SiLU  363 us  1.13 PFLOP/s: a pair's 14 items of 48 stages, about
+//                                1075 cycles a stage.  Its steps take 512 (8 of 256 x
+//                                128 x 16 a pair), the widening alone 447 a CTA: what a
+//                                stage waits for besides is not known
+//   512 rows each        890 us  1.85 PFLOP/s, the measured rate of the tensor cores
+// and 64 of 6144 x 2048 with 256 rows each 292 us, 1.41 PFLOP/s: the tensor cores stand
+// still while an item of more than 128 positions is stored, which has both parts of
+// the sums.  Few planes (8 of 4096 x 6144 make 128 items, two rounds of the 76 pairs)
+// are bound by what one pair takes in, a stage of 256 columns in 1240 cycles: 42 us
+// where their bytes take 30.
+//
+// The tensor cores' fp32 sums cut off what does not fit instead of rounding it, as
+// they do in a library's bf16 product: at 2048 columns 0.11 % of the outputs are the
+// bf16 value next to the one that the exact sum rounds to, at 6144 0.34 %, as many as
+// the library's (with every addition rounded to fp32: 0.03 and 0.05 %).
 //
 // Every wait is bounded; one that gave up sets the status word, and each copying
 // warp waits for its own copies before the CTA leaves.
@@ -833,8 +842,11 @@ template <bool kFp8, bool kSilu>
 cudaError_t launch_sized(const GroupedArgs &a, int sms, cudaStream_t s)
 {
     // Positions of an item: more take the weights fewer times, fewer leave room for
-    // more and longer stages.  The host knows the mean, and groups are uneven as a
-    // rule.  Items of up to 64 / 128 / 256, 64 planes of 4096 x 6144 E4M3, SiLU, us:
+    // more and longer stages.  The host knows a mean only, and groups are uneven as a
+    // rule; rows of no group count in it, and groups without rows do, so that where
+    // most rows lie elsewhere items are too large for what is here (at 32 rows 314 us
+    // for 258), and where few of the groups are hit too small (128 rows, 491 for 364).
+    // Items of up to 64 / 128 / 256, 64 planes of 4096 x 6144 E4M3, SiLU, us:
     //   rows a group      all alike          uneven (a twelfth to twice the mean)
     //   32             258 / 297 / 314             292 / 300 / 320
     //   48             267 / 301 / 322             345 / 303 / 324

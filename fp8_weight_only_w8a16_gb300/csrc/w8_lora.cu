@@ -4,8 +4,8 @@
 // Two launches.  The first makes v = A x in fp32: a CTA takes 16 positions of
 // one adapter and a range of k, its warps taking 32-column blocks in turn; the
 // ranges' partial sums go to the workspace, [range][position][rank].  The
-// second adds them in order and multiplies by B: a CTA takes 16 or 64
-// positions of one adapter and a run of columns.  Both products are on
+// second adds them in order and multiplies by B: a CTA takes 16 positions of
+// one adapter and a run of columns.  Both products are on
 // tensor-core steps (mma.sync m16n8k16), far below their rate: the operator is
 // bound by its bytes (x, the adapters, y twice), and with few rows by its two
 // launches.  Where adapters have rows enough, tiles of 128 positions go through
@@ -889,8 +889,17 @@ cudaError_t lora(const w8_lora &a, float *v, int sms, cudaStream_t s)
     if (fast && a.n_rows >= (kWide ? 256 : 1024) && a.n_rows >= (kWide ? 32 : 64) * int64_t(a.n_adapters)) {
         constexpr int kRank = kTiles <= 4 ? 64 : 128;
         // The first product by tiles of 16 reads A once for each of them, which for a
-        // small A costs less than the ranges' join: 4099 rows of 2048 columns at rank 16
-        // 63 us instead of 67, at rank 64 66 and 66; of 16384 at rank 32 92 instead of 62.
+        // small A costs less than the ranges' join.  4099 rows of 5 adapters, tiles of 16 /
+        // of 128, us, by rank x k (16, 32, 64 or 128 of rank) of
+        //   32768   rank 16 of 2048 to 16384                62.3 / 65.5
+        //   65536   rank 64 of 1024 to 16384                64.4 / 65.2
+        //   131072  rank 64 of 2048 to 16384                69.6 / 70.4
+        //           rank 32 of 4096 to 6144                 43.7 / 44.3
+        //           rank 16 of 8192 to 6144                 56.7 / 49.2
+        //           rank 128 of 1024 to 6144                56.7 / 44.7
+        //   262144  rank 64 of 4096 to 6144                 50.2 / 47.5
+        //           rank 32 of 8192 to 6144                 60.3 / 51.6
+        //           rank 128 of 2048 to 6144                74.1 / 49.6
         const bool small = int64_t(16 * kTiles) * a.k < 131072;
         const cudaError_t e = small ? shrink<kTiles>(a, v, splits, s) : shrink_tc<kRank>(a, v, 16 * kTiles, sms, s);
         return e != cudaSuccess ? e : expand_tc<kRank>(a, v, 16 * kTiles, sms, small ? splits : 0, s);

@@ -68,8 +68,9 @@ w8_status w8_grouped_device_status(int *status, int reset);
  *     the lowest number first among equal ones;
  *   weights[t][j] = scale * p of ids[t][j], with `normalize` divided by the
  *     sum of the chosen p.
- * The order is that of the exact c_e: where fp32 cannot tell two of them apart
- * they are computed again in 64 bits.  Weights are fp32 throughout.
+ * The order is that of c_e in 64 bits: where fp32 cannot tell two of them apart
+ * they are computed again (those that 64 bits cannot tell apart are equal).
+ * Weights are fp32 throughout.
  * An expert whose logit (or bias) is -inf or NaN is never chosen and adds
  * nothing; a token with fewer than `top` experts left gets id -1 and weight 0
  * in the remaining places.  A logit of +inf gives NaN weights with softmax.
@@ -165,7 +166,8 @@ w8_status w8_expert_sum(const uint16_t *y, int64_t ldy, const int32_t *ids, cons
  *   v = A_a x[t]  (rank_a sums over k, fp32)
  *   out[t][c] = bf16( y[t][c] + scales[a] sum_j B_a[c][j] v_j ),  c < n.
  * v enters the second product as the sum of two bf16 values, so that nothing
- * of it is lost above 2^-16; all sums are fp32.  Rows that no position names
+ * of it is lost above 2^-16 (an infinity in B may give NaN: one of the two may
+ * be 0); all sums are fp32.  Rows that no position names
  * are not written; a row outside 0 .. n_tok - 1 is skipped.  Of two positions
  * with one row either's result is left (with out on y perhaps both added): a
  * token has one adapter.
