@@ -54,6 +54,7 @@
 #include "w8_internal.h"
 #include "w8_sum_parts.h"
 #include "w8_tcgen.cuh"
+#include "w8_turns.h"
 
 namespace w8 {
 
@@ -104,7 +105,7 @@ static_assert(fits(0, 0) && fits(0, 1) && fits(0, 2) && fits(1, 0) && fits(1, 1)
 struct Shared {
     uint64_t full_w[kMaxW], empty_w[kMaxW];
     uint64_t full_x[kMaxX], free_x[kMaxX];
-    uint64_t ready[kMaxA], used[kMaxA]; // A and x of a stage are in place (both CTAs'; in the first), A is used
+    uint64_t ready[kMaxA], used[2 * kMaxA]; // A and x of a stage are in place (both CTAs'; in the first), A is used
     uint64_t sums[2], sums_read[2], end; // of the two parts
     int start[W8_MAX_GROUPS + 1];     // first position of each group
     int tiles[W8_MAX_GROUPS];         // position tiles up to and with each group
@@ -113,25 +114,13 @@ struct Shared {
 };
 static_assert(kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
 
-// Slots of a ring in turn, and the parity of their use.
-struct Turn {
-    int n = 0, k = 0;    // uses so far, the next slot
-    uint32_t parity = 0;
-    __device__ __forceinline__ void step(int slots)
-    {
-        ++n;
-        if (++k == slots) {
-            k = 0;
-            parity ^= 1u;
-        }
-    }
-};
-// Waits for the last use of every slot.
-__device__ __forceinline__ bool wait_last(uint64_t *bars, int slots, int uses)
+// Waits for the last use of every slot, on `round` barriers (one a slot, if not said).
+__device__ __forceinline__ bool wait_last(uint64_t *bars, int slots, int uses, int round = 0)
 {
     bool ok = true;
+    round = round ? round : slots;
     for (int i = max(uses - slots, 0); i < uses; ++i)
-        ok = bar_wait(&bars[i % slots], uint32_t(i / slots) & 1u) && ok;
+        ok = bar_wait(&bars[i % round], uint32_t(i / round) & 1u) && ok;
     return ok;
 }
 
@@ -315,6 +304,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
     constexpr int kRun = run_bytes(kFp8), kStageW = stage_w(kFp8, cfg), kStageX = stage_x(cfg);
     constexpr int kChunks = cfg.blocks / 2, kChunkX = cfg.most / 2 * 128; // 64 columns of a CTA's positions
     constexpr int kPart = part_cols(cfg), kACol = 2 * kPart;
+    constexpr int kUsed = used_bars(cfg.a);                              // barriers of A's uses
     constexpr int kBoxBlocks = 2048 / kRun;                              // K blocks of a box of weights
     extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ __align__(16) Shared sh;
@@ -334,7 +324,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
         }
         for (int i = 0; i < kMaxA; ++i) {
             bar_init(&sh.ready[i], 2 * 4);
-            bar_init(&sh.used[i], 1);
+            bar_init(&sh.used[2 * i], 1);
+            bar_init(&sh.used[2 * i + 1], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&sh.sums[i], 1);
@@ -530,14 +521,14 @@ __global__ void __launch_bounds__(kGpThreads, 1)
         if (h == 0) {
             // The steps' last arrivals come to both CTAs, which may not leave before.
             if (fine)
-                ok = wait_last(sh.free_x, cfg.x, to.n) && wait_last(sh.used, cfg.a, to.n) && ok;
+                ok = wait_last(sh.free_x, cfg.x, to.n) && wait_last(sh.used, cfg.a, to.n, kUsed) && ok;
             ok = bar_wait(&sh.end, 0) && ok;
         }
     } else if (warp == kWarpIssue) {
         if (rank == 0) {
             const uint64_t b0 = desc128_k(smem_addr(s_x), 1024);
             Turn ta;              // of A
-            int kx = 0;           // slot of x
+            int kx = 0, ku = 0;   // slot of x, barrier of A's use
             Parts parts;
             for (Item it = item(); it.group >= 0 && ok; id += pairs, it = item()) {
                 parts.take(it.n, kPart);
@@ -557,7 +548,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                         fence_after();
                         const uint64_t b = b0 + uint64_t((kx * kStageX) >> 4);
                         const uint32_t at = uint32_t(kACol + ta.k * 16 * cfg.blocks);
-                        const int now = ta.k, nb = p.kb - st * cfg.blocks;
+                        const int use = kUsed == cfg.a ? ta.k : ku, nb = p.kb - st * cfg.blocks;
                         ta.step(cfg.a);
                         there = bar_done(&sh.ready[ta.k], ta.parity);
                         for (int c = 0; c < kChunks; ++c) {
@@ -569,7 +560,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                                     pair_mma_ts(sums, at + uint32_t(c * 32 + q * 8), b + uint64_t((c * kChunkX + q * 32) >> 4), idesc,
                                                 uint32_t(st | c | q));
                         }
-                        pair_commit(&sh.used[now]);
+                        pair_commit(&sh.used[use]);
+                        ku = ku + 1 == kUsed ? 0 : ku + 1;
                         pair_commit(&sh.free_x[kx]);
                         kx = kx + 1 == cfg.x ? 0 : kx + 1;
                     }
@@ -593,6 +585,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                 parts.done();
                 ok = __shfl_sync(0xffffffffu, ok, who);
                 kx = __shfl_sync(0xffffffffu, kx, who);
+                ku = __shfl_sync(0xffffffffu, ku, who);
                 ta.k = __shfl_sync(0xffffffffu, ta.k, who);
                 ta.parity = __shfl_sync(0xffffffffu, ta.parity, who);
             }
@@ -609,16 +602,17 @@ __global__ void __launch_bounds__(kGpThreads, 1)
         const uint32_t at0 = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(kACol);
         const uint32_t ready0 = in_first(&sh.ready[0]);
         // A barrier's phase may be waited for only once the one before has ended.  The
-        // two turns run apart; that A's stage s - cfg.a is used says that all its
-        // operands and those before had come, so a turn waits for that first, and the
-        // rings of weights and x have at least as many slots.
-        Turn ta, tw, tx;
+        // two turns run apart; that A's stage s - cfg.a is used (of whose barriers each
+        // turn sees every phase: w8_turns.h) says that all its operands and those before
+        // had come, so a turn waits for that first, and the rings of weights and x have at
+        // least as many slots.
+        Turn ta, tu, tw, tx; // tu: the use of the stage cfg.a before, where its barriers are not the slots'
         for (Item it = item(); it.group >= 0 && ok; id += pairs, it = item()) {
             for (int st = 0; st < stages; ++st) {
                 if ((ta.n & 1) == turn) {
                     auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity); };
                     if (ta.n >= cfg.a)
-                        ok = wait(&sh.used[ta.k], ta.parity ^ 1u);
+                        ok = kUsed == cfg.a ? wait(&sh.used[ta.k], ta.parity ^ 1u) : wait(&sh.used[tu.k], tu.parity);
                     ok = ok && wait(&sh.full_w[tw.k], tw.parity);
                     if (!ok)
                         break;
@@ -662,6 +656,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                     if (lane == 0)
                         pair_arrive(ready0 + uint32_t(8 * ta.k));
                 }
+                if (ta.n >= cfg.a)
+                    tu.step(kUsed);
                 ta.step(cfg.a);
                 tw.step(cfg.w);
                 tx.step(cfg.x);
