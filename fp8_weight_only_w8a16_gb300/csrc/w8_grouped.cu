@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
     constexpr int kChunks = cfg.blocks / 2, kChunkX = cfg.most / 2 * 128; // 64 columns of a CTA's positions
     constexpr int kPart = part_cols(cfg), kACol = 2 * kPart;
     constexpr int kUsed = used_bars(cfg.a);                              // barriers of A's uses
+    constexpr bool kSlots = kUsed == cfg.a;                              // they are the slots' (no counts of their own)
     constexpr int kBoxBlocks = 2048 / kRun;                              // K blocks of a box of weights
     extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ __align__(16) Shared sh;
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                         fence_after();
                         const uint64_t b = b0 + uint64_t((kx * kStageX) >> 4);
                         const uint32_t at = uint32_t(kACol + ta.k * 16 * cfg.blocks);
-                        const int use = kUsed == cfg.a ? ta.k : ku, nb = p.kb - st * cfg.blocks;
+                        const int use = kSlots ? ta.k : ku, nb = p.kb - st * cfg.blocks;
                         ta.step(cfg.a);
                         there = bar_done(&sh.ready[ta.k], ta.parity);
                         for (int c = 0; c < kChunks; ++c) {
@@ -561,7 +562,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                                                 uint32_t(st | c | q));
                         }
                         pair_commit(&sh.used[use]);
-                        ku = ku + 1 == kUsed ? 0 : ku + 1;
+                        if constexpr (!kSlots)
+                            ku = ku + 1 == kUsed ? 0 : ku + 1;
                         pair_commit(&sh.free_x[kx]);
                         kx = kx + 1 == cfg.x ? 0 : kx + 1;
                     }
@@ -585,7 +587,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                 parts.done();
                 ok = __shfl_sync(0xffffffffu, ok, who);
                 kx = __shfl_sync(0xffffffffu, kx, who);
-                ku = __shfl_sync(0xffffffffu, ku, who);
+                if constexpr (!kSlots)
+                    ku = __shfl_sync(0xffffffffu, ku, who);
                 ta.k = __shfl_sync(0xffffffffu, ta.k, who);
                 ta.parity = __shfl_sync(0xffffffffu, ta.parity, who);
             }
@@ -606,13 +609,13 @@ __global__ void __launch_bounds__(kGpThreads, 1)
         // turn sees every phase: w8_turns.h) says that all its operands and those before
         // had come, so a turn waits for that first, and the rings of weights and x have at
         // least as many slots.
-        Turn ta, tu, tw, tx; // tu: the use of the stage cfg.a before, where its barriers are not the slots'
+        Turn ta, tu, tw, tx; // tu: the use of the stage cfg.a before (unless kSlots)
         for (Item it = item(); it.group >= 0 && ok; id += pairs, it = item()) {
             for (int st = 0; st < stages; ++st) {
                 if ((ta.n & 1) == turn) {
                     auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity); };
                     if (ta.n >= cfg.a)
-                        ok = kUsed == cfg.a ? wait(&sh.used[ta.k], ta.parity ^ 1u) : wait(&sh.used[tu.k], tu.parity);
+                        ok = kSlots ? wait(&sh.used[ta.k], ta.parity ^ 1u) : wait(&sh.used[tu.k], tu.parity);
                     ok = ok && wait(&sh.full_w[tw.k], tw.parity);
                     if (!ok)
                         break;
@@ -656,8 +659,9 @@ __global__ void __launch_bounds__(kGpThreads, 1)
                     if (lane == 0)
                         pair_arrive(ready0 + uint32_t(8 * ta.k));
                 }
-                if (ta.n >= cfg.a)
-                    tu.step(kUsed);
+                if constexpr (!kSlots)
+                    if (ta.n >= cfg.a)
+                        tu.step(kUsed);
                 ta.step(cfg.a);
                 tw.step(cfg.w);
                 tx.step(cfg.x);

@@ -94,9 +94,11 @@ def test_the_kernel_waits_so():
     text = open(os.path.join(CSRC, "w8_grouped.cu")).read()
     assert "constexpr int kUsed = used_bars(cfg.a);" in text
     # (as many barriers as slots: the slot's own, the phase of the lap before)
-    assert "const int use = kUsed == cfg.a ? ta.k : ku," in text
-    assert "pair_commit(&sh.used[use]);\n                        ku = ku + 1 == kUsed ? 0 : ku + 1;" in text
-    assert "ok = kUsed == cfg.a ? wait(&sh.used[ta.k], ta.parity ^ 1u) : wait(&sh.used[tu.k], tu.parity);" in text
-    assert "if (ta.n >= cfg.a)\n                    tu.step(kUsed);\n                ta.step(cfg.a);" in text
+    assert "constexpr bool kSlots = kUsed == cfg.a;" in text and "const int use = kSlots ? ta.k : ku," in text
+    assert ("pair_commit(&sh.used[use]);\n                        if constexpr (!kSlots)\n                            "
+            "ku = ku + 1 == kUsed ? 0 : ku + 1;") in text
+    assert "ok = kSlots ? wait(&sh.used[ta.k], ta.parity ^ 1u) : wait(&sh.used[tu.k], tu.parity);" in text
+    assert ("if constexpr (!kSlots)\n                    if (ta.n >= cfg.a)\n                        tu.step(kUsed);\n"
+            "                ta.step(cfg.a);") in text
     assert "wait_last(sh.used, cfg.a, to.n, kUsed)" in text
     assert text.count("sh.used") == 6  # the four above, and the two that set them up
