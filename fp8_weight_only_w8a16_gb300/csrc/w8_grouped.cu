@@ -27,12 +27,12 @@
 // power limit).  64 planes of 4096 x 6144 E4M3 (1.6 GB):
 //   2 rows each, SiLU    255 us  6.3 TB/s of HBM (bf16 planes 7.2), tensor cores 16 %
 //                                of the time
-//   128 rows each, SiLU  363 us  1.13 PFLOP/s: a pair's 14 items of 48 stages, about
+//   128 rows each, SiLU  365 us  1.13 PFLOP/s: a pair's 14 items of 48 stages, about
 //                                1075 cycles a stage.  Its steps take 512 (8 of 256 x
 //                                128 x 16 a pair), the widening alone 447 a CTA: what a
 //                                stage waits for besides is not known
-//   512 rows each        890 us  1.85 PFLOP/s, the measured rate of the tensor cores
-// and 64 of 6144 x 2048 with 256 rows each 292 us, 1.41 PFLOP/s: the tensor cores stand
+//   512 rows each        900 us  1.83 PFLOP/s, near the measured rate of the tensor cores
+// and 64 of 6144 x 2048 with 256 rows each 296 us, 1.39 PFLOP/s: the tensor cores stand
 // still while an item of more than 128 positions is stored, which has both parts of
 // the sums.  Few planes (8 of 4096 x 6144 make 128 items, two rounds of the 76 pairs)
 // are bound by what one pair takes in, a stage of 256 columns in 1240 cycles: 42 us
